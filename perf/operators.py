@@ -207,6 +207,8 @@ def prepare(case, seed):
                                          case["cache"], case.get("causal", False))
         if op == "tree":
             st["decoder"] = mla.TreeDecoder(st["shape"])
+        if op == "weights":
+            st["attn"] = mla.AttnWeights(st["shape"])
         if op == "compact":
             st["compactor"] = mla.CacheCompactor(st["shape"], st["src"].shape[1])
     return st
@@ -360,8 +362,8 @@ def _own_tree(st):
 
 
 def _own_weights(st):
-    st["mla"].mla_attn_weights(st["shape"], st["q"], st["pool"], st["scale"], st["table"], st["seqlens"], st["lse"], SCALE,
-                               st["case"]["decay"], st["weights"])
+    st["attn"].accumulate(st["q"], st["pool"], st["table"], st["seqlens"], st["lse"], SCALE, st["case"]["decay"],
+                          st["weights"], kv_scale=st["scale"])
     return st["weights"]
 
 
