@@ -16,8 +16,12 @@
  *
  * Around the decode: the query absorption and the output decompression
  * (mla_absorb_q, mla_decompress_o), token-level sparse decode over listed
- * cache positions (mla_sparse_*), and the MLAvar6+ split decode with the
- * newest tokens held decompressed (mla_var6_*).
+ * cache positions (mla_sparse_*), the MLAvar6+ split decode with the
+ * newest tokens held decompressed (mla_var6_*), attention for trees of
+ * drafted tokens (mla_tree_*), and what cuts a cache to a budget or closes
+ * up an accepted path: the attention weight each token received
+ * (mla_attn_weights_fwd), the choice of what stays (mla_evict_select) and the
+ * move of the cache rows (mla_cache_compact).
  *
  * Conventions shared by every call
  *  - All tensor pointers are DEVICE pointers owned by the caller.  The
@@ -49,7 +53,7 @@ enum {
   MLA_ERR_WORKSPACE = -3,    /* workspace / schedule buffer too small          */
   MLA_ERR_CUDA = -4,         /* a CUDA runtime call failed (launch, attribute) */
   MLA_ERR_TIMEOUT = -5,      /* device status: a bounded wait gave up          */
-  MLA_ERR_DEVICE_CHECK = -6  /* device status: seqlen / page id out of range,
+  MLA_ERR_DEVICE_CHECK = -6  /* device status: a length, page id or list entry out of range,
                                 or a value row outside fp16's range            */
 };
 
@@ -264,6 +268,125 @@ int mla_var6_decode_fwd(const mla_shape_t* shape, int n_new, const void* qz, con
 /* Device status of the split decode's kernels; as mla_get_device_status. */
 int mla_var6_get_device_status(const mla_shape_t* shape, int n_new, int num_sms, void* workspace, void* stream,
                                int* status);
+
+/* ---- attention for a tree of drafted tokens ---------------------------------
+ * A speculative step whose drafted tokens form a tree (or any other relation)
+ * in the place of a chain.  Request r holds t = seqlens[r] cached tokens, of
+ * which the last n = draft_lens[r] are drafted: node i lies at position
+ * t - n + i and is query token i.  It sees every position before t - n and,
+ * among the drafted tokens, exactly those whose bit is set in its mask row:
+ * node d is bit d % 64 of word d / 64.  Bits from n on count for nothing, and
+ * a node sees itself only if its own bit says so.  S, O and lse as for
+ * mla_decode_fwd; a query token i >= n, and a node that sees no position, get
+ * O = 0 and lse = -inf.
+ *   shape     : as for mla_decode_fwd, causal = 0; s_q is the number of node
+ *               slots per request (the mask says what each sees).
+ *   draft_lens: device int32 [batch], or NULL: min(s_q, t) nodes.  A count
+ *               outside [0, min(s_q, t)] is clamped and flagged.
+ *   tree_mask : device int64 [batch, s_q, ceil(s_q / 64)], 8-byte aligned.
+ *   q, kv_cache, kv_scale, block_table, seqlens, softmax_scale, out, lse: as
+ *               for mla_decode_fwd, with its condition on the value rows.
+ *   workspace : mla_tree_workspace_bytes(shape, num_sms of this device)
+ *               bytes, 256-byte aligned, zero-filled before its first use (it
+ *               holds the schedule and the status word); the caller must not
+ *               touch it while the call's work runs, and calls that may
+ *               overlap in time need one each. */
+size_t mla_tree_workspace_bytes(const mla_shape_t* shape, int num_sms);
+int mla_tree_decode_fwd(const mla_shape_t* shape, const void* q, const void* kv_cache, const float* kv_scale,
+                        const int32_t* block_table, const int32_t* seqlens, const int32_t* draft_lens,
+                        const int64_t* tree_mask, float softmax_scale, void* workspace, size_t workspace_bytes,
+                        void* out, float* lse, void* stream);
+/* Device status of the tree decode's kernels; as mla_get_device_status. */
+int mla_tree_get_device_status(const mla_shape_t* shape, int num_sms, void* workspace, void* stream, int* status);
+
+/* Mask rows of trees given by their parents: bit d of row i is set when node
+ * d is i or an ancestor of i.
+ *   parents   : device int32 [batch, s_q]; parents[r][i] < i is node i's
+ *               parent, or -1 where its path meets the committed prefix.  A
+ *               parent outside [-1, i) counts as -1.
+ *   draft_lens: device int32 [batch] or NULL (s_q): rows from draft_lens[r] on
+ *               are zero and their parents are not read.  A count outside
+ *               [0, s_q] is clamped.
+ *   tree_mask : device int64 [batch, s_q, ceil(s_q / 64)], written entirely.
+ *   device_status: optional device int32 that a bad parent or count ORs a
+ *               nonzero bit into (never cleared by this call).
+ * batch <= 65535, s_q <= 2^20. */
+int mla_tree_mask(int32_t batch, int32_t s_q, const int32_t* parents, const int32_t* draft_lens, int64_t* tree_mask,
+                  int32_t* device_status, void* stream);
+
+/* ---- eviction by attention weight --------------------------------------------
+ * The weight that each cached token received, accumulated over steps:
+ *   weights[r][j] = decay * weights[r][j]
+ *                 + sum over (i, h), token i seeing j, of
+ *                   exp(softmax_scale * q[r][i][h] . C_j - lse[r][i][h])
+ * for j < seqlens[r]; later entries are left as they were.  Which positions
+ * query token i sees is the shape's causal rule (mla_decode_fwd).  lse is the
+ * decode's output for the same q, cache and scale.  A row whose lse is -inf
+ * adds nothing, whatever its q holds (so padded query tokens can be marked).
+ * decay = 0 does not read the old weights.  The sums are fp32, in an order
+ * that does not change from call to call.
+ *   shape, q, kv_cache, kv_scale, block_table, seqlens, softmax_scale: as for
+ *             mla_decode_fwd; batch <= 65535.
+ *   lse     : fp32 [batch, s_q, num_heads].
+ *   weights : fp32 [batch, max_pages_per_seq * 64].
+ *   workspace: mla_attn_weights_workspace_bytes(shape, num_sms of this device)
+ *             bytes, 256-byte aligned, zero-filled before its first use (it
+ *             holds the status word); the caller must not touch it while the
+ *             call's work runs, and calls that may overlap in time need one
+ *             each.
+ * Tokens of a page whose id is out of range receive nothing (flagged). */
+size_t mla_attn_weights_workspace_bytes(const mla_shape_t* shape, int num_sms);
+int mla_attn_weights_fwd(const mla_shape_t* shape, const void* q, const void* kv_cache, const float* kv_scale,
+                         const int32_t* block_table, const int32_t* seqlens, const float* lse, float softmax_scale,
+                         float decay, float* weights, void* workspace, size_t workspace_bytes, void* stream);
+/* Reads and clears the device status of the kernels that used this workspace;
+ * SYNCHRONISES `stream`. */
+int mla_attn_weights_get_device_status(void* workspace, void* stream, int* status);
+
+/* Which tokens of each request stay in a cache of at most `budget` tokens:
+ * the first `sink`, the last `recent` and, of those between, the
+ * budget - sink - recent with the largest weights (of equal weights the
+ * lowest positions; NaN counts as less than every number).  A request of at
+ * most `budget` tokens keeps them all.
+ *   max_tokens: row length of weights; seqlens outside [0, max_tokens] are
+ *             clamped and flagged.
+ *   weights : fp32 [batch, max_tokens]; entries from seqlens[r] on not read.
+ *   budget >= 1, sink >= 0, recent >= 0, sink + recent <= budget.
+ *   kept    : int32 [batch, budget], the kept positions in ascending order,
+ *             then -1 (the form of mla_sparse_decode_fwd's lists).
+ *   kept_lens: int32 [batch], min(seqlens[r], budget).
+ *   device_status: optional device int32 that a length out of range ORs a
+ *             nonzero bit into (never cleared by this call). */
+int mla_evict_select(int32_t batch, int32_t max_tokens, const float* weights, const int32_t* seqlens, int32_t budget,
+                     int32_t sink, int32_t recent, int32_t* kept, int32_t* kept_lens, int32_t* device_status,
+                     void* stream);
+
+/* Moves cache rows towards the front of their request's own pages, in place:
+ * the row at position src[r][k] goes to position base + k for k < src_lens[r],
+ * base = base[r] (NULL: 0).  Serves an eviction (src = kept, base NULL) and
+ * the accepted path of a drafted tree (src = its positions, base = the
+ * committed length).  Rows that no destination covers are left as they were;
+ * the caller then uses base + src_lens[r] as the request's length.
+ *   shape   : the cache's (s_q and num_heads are not used).
+ *   src     : int32 [batch, max_rows]; the first src_lens[r] of a row ascend
+ *             strictly, with base + k <= src[r][k] < max_pages_per_seq * 64.
+ *             An entry that does not, or whose page id is out of range, is
+ *             not moved and flagged; the request's rows are then not valid.
+ *   src_lens: int32 [batch]; outside [0, max_rows]: clamped and flagged.
+ *   base    : int32 [batch] or NULL.  Negative: flagged, nothing moved.
+ *   weights : fp32 [batch, max_pages_per_seq * 64] or NULL; moved as the rows.
+ *   kv_scale: FP8 cache: moved as the rows.
+ *   workspace: mla_compact_workspace_bytes(shape, max_rows) bytes, 256-byte
+ *             aligned, zero-filled before its first use; calls that may
+ *             overlap in time need one each.
+ * A page that two requests share (or one request lists twice) must lie where
+ * nothing moves: before the first entry with src[r][k] != base + k. */
+size_t mla_compact_workspace_bytes(const mla_shape_t* shape, int max_rows);
+int mla_cache_compact(const mla_shape_t* shape, void* kv_cache, float* kv_scale, const int32_t* block_table,
+                      const int32_t* src, const int32_t* src_lens, const int32_t* base, int32_t max_rows, float* weights,
+                      void* workspace, size_t workspace_bytes, void* stream);
+/* Reads and clears the compaction's device status; SYNCHRONISES `stream`. */
+int mla_compact_get_device_status(void* workspace, void* stream, int* status);
 
 /* ---- the projections on either side of the decode -------------------------
  * "MLA Cost Analysis & Regime Guide", section "Absorption Trick": the key

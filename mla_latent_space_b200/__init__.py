@@ -86,6 +86,28 @@ def lib() -> ctypes.CDLL:
         L.mla_absorb_q.restype = i32
         L.mla_decompress_o.argtypes = [i32, i32, vp, vp, vp, vp, vp]
         L.mla_decompress_o.restype = i32
+        L.mla_tree_mask.argtypes = [i32, i32, vp, vp, vp, vp, vp]
+        L.mla_tree_mask.restype = i32
+        L.mla_tree_workspace_bytes.argtypes = [sp, i32]
+        L.mla_tree_workspace_bytes.restype = sz
+        L.mla_tree_decode_fwd.argtypes = [sp, vp, vp, vp, vp, vp, vp, vp, f32, vp, sz, vp, vp, vp]
+        L.mla_tree_decode_fwd.restype = i32
+        L.mla_tree_get_device_status.argtypes = [sp, i32, vp, vp, ctypes.POINTER(i32)]
+        L.mla_tree_get_device_status.restype = i32
+        L.mla_attn_weights_workspace_bytes.argtypes = [sp, i32]
+        L.mla_attn_weights_workspace_bytes.restype = sz
+        L.mla_attn_weights_fwd.argtypes = [sp, vp, vp, vp, vp, vp, vp, f32, f32, vp, vp, sz, vp]
+        L.mla_attn_weights_fwd.restype = i32
+        L.mla_attn_weights_get_device_status.argtypes = [vp, vp, ctypes.POINTER(i32)]
+        L.mla_attn_weights_get_device_status.restype = i32
+        L.mla_evict_select.argtypes = [i32, i32, vp, vp, i32, i32, i32, vp, vp, vp, vp]
+        L.mla_evict_select.restype = i32
+        L.mla_compact_workspace_bytes.argtypes = [sp, i32]
+        L.mla_compact_workspace_bytes.restype = sz
+        L.mla_cache_compact.argtypes = [sp, vp, vp, vp, vp, vp, vp, i32, vp, vp, sz, vp]
+        L.mla_cache_compact.restype = i32
+        L.mla_compact_get_device_status.argtypes = [vp, vp, ctypes.POINTER(i32)]
+        L.mla_compact_get_device_status.restype = i32
         L.mla_error_string.argtypes = [i32]
         L.mla_error_string.restype = ctypes.c_char_p
         L.mla_version.argtypes = []
@@ -307,6 +329,152 @@ class Var6Decoder:
         _check(lib().mla_var6_get_device_status(ctypes.byref(self.shape), self.n_new, self.n_sms,
                                                 _ptr(self.workspace), _stream(stream), ctypes.byref(st)),
                "mla_var6_get_device_status")
+        return int(st.value)
+
+
+class TreeDecoder:
+    """Attention for trees of drafted tokens through the C ABI: holds the
+    zero-filled workspace (schedule, partial results, status) for one shape
+    and device.  ``tree_mask`` is int64 [b, s_q, ceil(s_q / 64)], as
+    mla_tree_mask writes it."""
+
+    def __init__(self, shape: mla_shape_t, device=None):
+        self.shape = shape
+        self.device = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
+        self.n_sms = num_sms(self.device)
+        nb = int(lib().mla_tree_workspace_bytes(ctypes.byref(shape), self.n_sms))
+        if nb == 0:
+            raise MLAError(-2, "TreeDecoder: shape not supported (causal must be 0)")
+        self.workspace = torch.zeros(nb, dtype=torch.uint8, device=self.device)
+
+    def decode(self, q, kv_cache, block_table, seqlens, tree_mask, softmax_scale, out, lse, draft_lens=None,
+               kv_scale=None, stream=None):
+        sh = self.shape
+        _check_decode_tensors(sh, q, kv_cache, kv_scale, block_table, seqlens, out, lse)
+        _need(tree_mask, "tree_mask", torch.int64, (sh.batch, sh.s_q, (sh.s_q + 63) // 64))
+        if draft_lens is not None:
+            _need(draft_lens, "draft_lens", torch.int32, (sh.batch,))
+        rc = lib().mla_tree_decode_fwd(ctypes.byref(sh), _ptr(q), _ptr(kv_cache), _ptr(kv_scale), _ptr(block_table),
+                                       _ptr(seqlens), _ptr(draft_lens), _ptr(tree_mask), float(softmax_scale),
+                                       _ptr(self.workspace), self.workspace.numel(), _ptr(out), _ptr(lse),
+                                       _stream(stream))
+        _check(rc, "mla_tree_decode_fwd")
+
+    def status(self, stream=None) -> int:
+        st = ctypes.c_int(0)
+        _check(lib().mla_tree_get_device_status(ctypes.byref(self.shape), self.n_sms, _ptr(self.workspace),
+                                                _stream(stream), ctypes.byref(st)), "mla_tree_get_device_status")
+        return int(st.value)
+
+
+def mla_tree_mask(parents, tree_mask, draft_lens=None, device_status: Optional[torch.Tensor] = None, stream=None):
+    """tree_mask int64 [b, s, ceil(s / 64)]: bit d % 64 of word d / 64 of row
+    i says whether drafted node d is i or an ancestor of i, from parents int32
+    [b, s] (-1: the committed prefix)."""
+    _need(parents, "parents", torch.int32)
+    if parents.dim() != 2:
+        raise ValueError(f"parents must have shape [batch, s_q], got {tuple(parents.shape)}")
+    b, s = parents.shape
+    _need(tree_mask, "tree_mask", torch.int64, (b, s, (s + 63) // 64))
+    if draft_lens is not None:
+        _need(draft_lens, "draft_lens", torch.int32, (b,))
+    if device_status is not None:
+        _need(device_status, "device_status", torch.int32)
+    _check(lib().mla_tree_mask(b, s, _ptr(parents), _ptr(draft_lens), _ptr(tree_mask), _ptr(device_status),
+                               _stream(stream)), "mla_tree_mask")
+
+
+class AttnWeights:
+    """The attention weight that each cached token receives, accumulated over
+    steps, through the C ABI: holds the zero-filled workspace for one shape
+    and device."""
+
+    def __init__(self, shape: mla_shape_t, device=None):
+        self.shape = shape
+        self.device = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
+        self.n_sms = num_sms(self.device)
+        nb = int(lib().mla_attn_weights_workspace_bytes(ctypes.byref(shape), self.n_sms))
+        if nb == 0:
+            raise MLAError(-2, "AttnWeights: shape not supported (batch <= 65535)")
+        self.workspace = torch.zeros(nb, dtype=torch.uint8, device=self.device)
+
+    def accumulate(self, q, kv_cache, block_table, seqlens, lse, softmax_scale, decay, weights, kv_scale=None,
+                   stream=None):
+        """weights[r, j] = decay * weights[r, j] + the attention weight that
+        the rows of q give cached token j (lse: the decode's output).  weights
+        fp32 [b, max_pages * 64], updated in place."""
+        sh = self.shape
+        _check_decode_tensors(sh, q, kv_cache, kv_scale, block_table, seqlens, None, lse)
+        _need(weights, "weights", torch.float32, (sh.batch, sh.max_pages_per_seq * PAGE))
+        rc = lib().mla_attn_weights_fwd(ctypes.byref(sh), _ptr(q), _ptr(kv_cache), _ptr(kv_scale), _ptr(block_table),
+                                        _ptr(seqlens), _ptr(lse), float(softmax_scale), float(decay), _ptr(weights),
+                                        _ptr(self.workspace), self.workspace.numel(), _stream(stream))
+        _check(rc, "mla_attn_weights_fwd")
+
+    def status(self, stream=None) -> int:
+        st = ctypes.c_int(0)
+        _check(lib().mla_attn_weights_get_device_status(_ptr(self.workspace), _stream(stream), ctypes.byref(st)),
+               "mla_attn_weights_get_device_status")
+        return int(st.value)
+
+
+def mla_evict_select(weights, seqlens, budget, sink, recent, kept, kept_lens,
+                     device_status: Optional[torch.Tensor] = None, stream=None):
+    """kept int32 [b, budget]: the positions that stay (the first `sink`, the
+    last `recent`, the heaviest between), ascending, then -1; kept_lens int32
+    [b].  weights fp32 [b, max_tokens]."""
+    _need(weights, "weights", torch.float32)
+    if weights.dim() != 2:
+        raise ValueError(f"weights must have shape [batch, max_tokens], got {tuple(weights.shape)}")
+    b = weights.shape[0]
+    _need(seqlens, "seqlens", torch.int32, (b,))
+    _need(kept, "kept", torch.int32, (b, int(budget)))
+    _need(kept_lens, "kept_lens", torch.int32, (b,))
+    if device_status is not None:
+        _need(device_status, "device_status", torch.int32)
+    _check(lib().mla_evict_select(b, weights.shape[1], _ptr(weights), _ptr(seqlens), int(budget), int(sink), int(recent),
+                                  _ptr(kept), _ptr(kept_lens), _ptr(device_status), _stream(stream)),
+           "mla_evict_select")
+
+
+class CacheCompactor:
+    """Moves cache rows to the front of their request's pages through the C
+    ABI (what an eviction kept, or an accepted path of drafted tokens).  Holds
+    the zero-filled workspace for one shape, list length and device."""
+
+    def __init__(self, shape: mla_shape_t, max_rows: int, device=None):
+        self.shape, self.max_rows = shape, int(max_rows)
+        self.device = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
+        nb = int(lib().mla_compact_workspace_bytes(ctypes.byref(shape), self.max_rows))
+        if nb == 0:
+            raise MLAError(-1, "CacheCompactor: invalid shape or list length")
+        self.workspace = torch.zeros(nb, dtype=torch.uint8, device=self.device)
+
+    def compact(self, kv_cache, block_table, src, src_lens, base=None, kv_scale=None, weights=None, stream=None):
+        sh = self.shape
+        if sh.cache_dtype == MLA_CACHE_BF16:
+            _need(kv_cache, "kv_cache", torch.bfloat16, (sh.num_pages, PAGE, D_QK))
+            if kv_scale is not None:
+                raise ValueError("kv_scale is only used with the fp8 cache")
+        else:
+            _need(kv_cache, "kv_cache", torch.uint8, (sh.num_pages, FP8_PAGE_BYTES))
+            _need(kv_scale, "kv_scale", torch.float32, (sh.num_pages, PAGE))
+        _need(block_table, "block_table", torch.int32, (sh.batch, sh.max_pages_per_seq))
+        _need(src, "src", torch.int32, (sh.batch, self.max_rows))
+        _need(src_lens, "src_lens", torch.int32, (sh.batch,))
+        if base is not None:
+            _need(base, "base", torch.int32, (sh.batch,))
+        if weights is not None:
+            _need(weights, "weights", torch.float32, (sh.batch, sh.max_pages_per_seq * PAGE))
+        rc = lib().mla_cache_compact(ctypes.byref(sh), _ptr(kv_cache), _ptr(kv_scale), _ptr(block_table), _ptr(src),
+                                     _ptr(src_lens), _ptr(base), self.max_rows, _ptr(weights), _ptr(self.workspace),
+                                     self.workspace.numel(), _stream(stream))
+        _check(rc, "mla_cache_compact")
+
+    def status(self, stream=None) -> int:
+        st = ctypes.c_int(0)
+        _check(lib().mla_compact_get_device_status(_ptr(self.workspace), _stream(stream), ctypes.byref(st)),
+               "mla_compact_get_device_status")
         return int(st.value)
 
 

@@ -37,6 +37,19 @@ int launch_absorb_q(int rows, int heads, const void* q, const void* w_k, void* q
                     cudaStream_t stream);
 int launch_decompress_o(int rows, int heads, const void* o_lat, const void* w_kvb2, void* out, int32_t* status,
                         cudaStream_t stream, const void* o_lat_lo = nullptr, void* out_lo = nullptr);
+cudaError_t launch_tree_mask(const int32_t* parents, const int32_t* draft_lens, int batch, int s_q, int64_t* mask,
+                             int32_t* status, cudaStream_t stream);
+size_t attn_weights_workspace_bytes(const mla_shape_t* shape, int num_sms);
+int launch_attn_weights(const mla_shape_t* shape, const void* q, const void* kv, const float* kv_scale,
+                        const int32_t* block_table, const int32_t* seqlens, const float* lse, float scale, float decay,
+                        float* weights, void* ws, int num_sms, cudaStream_t stream);
+cudaError_t launch_evict_select(const float* weights, int64_t max_tokens, const int32_t* seqlens, int batch, int budget,
+                                int sink, int recent, int32_t* kept, int32_t* kept_lens, int32_t* status,
+                                cudaStream_t stream);
+size_t compact_workspace_bytes(int batch, int max_rows);
+int launch_compact(const mla_shape_t* shape, void* kv, float* kv_scale, const int32_t* block_table, const int32_t* src,
+                   const int32_t* src_lens, const int32_t* base, int max_rows, float* weights, void* ws,
+                   cudaStream_t stream);
 }  // namespace mla
 
 using namespace mla;
@@ -212,6 +225,35 @@ bool var6_layout(const mla_shape_t* s, int n_new, int num_sms, Var6Layout* L) {
   off = up(off + rows * MLA_D_HEAD * 2);
   L->total = off;
   return true;
+}
+
+// Workspace of the tree decode: the schedule, then the decode workspace
+// (both 256-byte aligned).
+struct TreeLayout {
+  size_t sched, sched_bytes, ws, ws_bytes, total;
+};
+
+bool tree_layout(const mla_shape_t* s, int num_sms, TreeLayout* L) {
+  if (check_shape(s) != MLA_OK || s->causal != 0 || num_sms < 1) return false;
+  L->sched = 0;
+  L->sched_bytes = sched_bytes_for(s, num_sms);
+  L->ws = (L->sched_bytes + 255) & ~size_t(255);
+  L->ws_bytes = kStatusBytes + size_t(max_slots_for(num_workers_for(num_sms))) * kSlotBytes;
+  L->total = L->ws + L->ws_bytes;
+  return true;
+}
+
+// Reads and clears the status word at the head of a workspace.
+int read_status_word(void* workspace, void* stream, int* status) {
+  if (!workspace || !status) return MLA_ERR_INVALID_ARG;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  int32_t word = 0;
+  if (cudaMemcpyAsync(&word, workspace, 4, cudaMemcpyDeviceToHost, st) != cudaSuccess) return MLA_ERR_CUDA;
+  if (cudaStreamSynchronize(st) != cudaSuccess) return MLA_ERR_CUDA;
+  if (cudaMemsetAsync(workspace, 0, 4, st) != cudaSuccess) return MLA_ERR_CUDA;
+  if (cudaStreamSynchronize(st) != cudaSuccess) return MLA_ERR_CUDA;
+  *status = (word & kStatusTimeout) ? MLA_ERR_TIMEOUT : word ? MLA_ERR_DEVICE_CHECK : MLA_OK;
+  return MLA_OK;
 }
 
 }  // namespace
@@ -455,6 +497,142 @@ int mla_var6_get_device_status(const mla_shape_t* shape, int n_new, int num_sms,
   if (!workspace || !status || !var6_layout(shape, n_new, num_sms, &L)) return MLA_ERR_INVALID_ARG;
   char* w = static_cast<char*>(workspace);
   return mla_get_device_status(w + L.sched, w + L.ws, stream, status);
+}
+
+int mla_tree_mask(int32_t batch, int32_t s_q, const int32_t* parents, const int32_t* draft_lens, int64_t* tree_mask,
+                  int32_t* device_status, void* stream) {
+  CallRange range_("mla_tree_mask");
+  if (batch < 1 || s_q < 1 || !parents || !tree_mask) return MLA_ERR_INVALID_ARG;
+  if (batch > 65535 || s_q > (1 << 20)) return MLA_ERR_UNSUPPORTED;
+  if (!aligned(parents, 4) || !aligned(draft_lens, 4) || !aligned(tree_mask, 8) || !aligned(device_status, 4))
+    return MLA_ERR_INVALID_ARG;
+  return launch_tree_mask(parents, draft_lens, batch, s_q, tree_mask, device_status,
+                          static_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? MLA_OK
+             : MLA_ERR_CUDA;
+}
+
+size_t mla_tree_workspace_bytes(const mla_shape_t* shape, int num_sms) {
+  TreeLayout L;
+  return tree_layout(shape, num_sms, &L) ? L.total : 0;
+}
+
+int mla_tree_decode_fwd(const mla_shape_t* shape, const void* q, const void* kv_cache, const float* kv_scale,
+                        const int32_t* block_table, const int32_t* seqlens, const int32_t* draft_lens,
+                        const int64_t* tree_mask, float softmax_scale, void* workspace, size_t workspace_bytes,
+                        void* out, float* lse, void* stream) {
+  CallRange range_("mla_tree_decode_fwd");
+  int rc = check_shape(shape);
+  if (rc != MLA_OK) return rc;
+  if (shape->causal != 0 || !tree_mask || !workspace || !aligned(tree_mask, 8) || !aligned(draft_lens, 4) ||
+      !aligned(workspace, 256))
+    return MLA_ERR_INVALID_ARG;
+  int sms = 0;
+  if ((rc = device_sms(&sms)) != MLA_OK) return rc;
+  TreeLayout L;
+  if (!tree_layout(shape, sms, &L)) return MLA_ERR_UNSUPPORTED;
+  char* w = static_cast<char*>(workspace);
+  void* sched = w + L.sched;
+  void* ws = w + L.ws;
+  rc = check_decode_args(shape, q, kv_cache, kv_scale, block_table, seqlens, softmax_scale, sched, ws, L.ws_bytes, out,
+                         lse);
+  if (rc != MLA_OK) return rc;
+  if (workspace_bytes < L.total) return MLA_ERR_WORKSPACE;
+  DecodePrepared prep;
+  if ((rc = prepare_decode_sm100(shape, q, kv_cache, &prep, true)) != MLA_OK) return rc;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  ShapeInfo si = shape_info(shape);
+  si.tree = 1;
+  si.draft_lens = draft_lens;
+  if (launch_schedule(seqlens, si, num_workers_for(sms), static_cast<int32_t*>(sched), st) != cudaSuccess)
+    return MLA_ERR_CUDA;
+  const TreeArgs tree{draft_lens, tree_mask, (shape->s_q + 63) / 64};
+  const int cap = cap_slots_for(L.ws_bytes);
+  rc = enqueue_decode_sm100(prep, shape, q, kv_cache, kv_scale, block_table, seqlens, softmax_scale, sched, ws, cap, out,
+                            lse, st, nullptr, 0, &tree);
+  if (rc != MLA_OK) return rc;
+  return launch_combine(sched, ws, out, lse, si.batch * si.tiles_per_req, cap, st) == cudaSuccess ? MLA_OK
+                                                                                                  : MLA_ERR_CUDA;
+}
+
+int mla_tree_get_device_status(const mla_shape_t* shape, int num_sms, void* workspace, void* stream, int* status) {
+  TreeLayout L;
+  if (!workspace || !status || !tree_layout(shape, num_sms, &L)) return MLA_ERR_INVALID_ARG;
+  char* w = static_cast<char*>(workspace);
+  return mla_get_device_status(w + L.sched, w + L.ws, stream, status);
+}
+
+size_t mla_attn_weights_workspace_bytes(const mla_shape_t* shape, int num_sms) {
+  if (check_shape(shape) != MLA_OK || shape->batch > 65535 || num_sms < 1) return 0;
+  return attn_weights_workspace_bytes(shape, num_sms);
+}
+
+int mla_attn_weights_fwd(const mla_shape_t* shape, const void* q, const void* kv_cache, const float* kv_scale,
+                         const int32_t* block_table, const int32_t* seqlens, const float* lse, float softmax_scale,
+                         float decay, float* weights, void* workspace, size_t workspace_bytes, void* stream) {
+  CallRange range_("mla_attn_weights_fwd");
+  int rc = check_shape(shape);
+  if (rc != MLA_OK) return rc;
+  if (!q || !kv_cache || !block_table || !seqlens || !lse || !weights || !workspace) return MLA_ERR_INVALID_ARG;
+  if (shape->cache_dtype == MLA_CACHE_FP8_E4M3 && !kv_scale) return MLA_ERR_INVALID_ARG;
+  if (!aligned(q, 16) || !aligned(kv_cache, 256) || !aligned(kv_scale, 4) || !aligned(block_table, 4) ||
+      !aligned(seqlens, 4) || !aligned(lse, 4) || !aligned(weights, 4) || !aligned(workspace, 256))
+    return MLA_ERR_INVALID_ARG;
+  if (!std::isfinite(softmax_scale) || !std::isfinite(decay)) return MLA_ERR_INVALID_ARG;
+  if (shape->batch > 65535) return MLA_ERR_UNSUPPORTED;
+  int sms = 0;
+  if ((rc = device_sms(&sms)) != MLA_OK) return rc;
+  if (workspace_bytes < mla_attn_weights_workspace_bytes(shape, sms)) return MLA_ERR_WORKSPACE;
+  return launch_attn_weights(shape, q, kv_cache, kv_scale, block_table, seqlens, lse, softmax_scale, decay, weights,
+                             workspace, sms, static_cast<cudaStream_t>(stream));
+}
+
+int mla_attn_weights_get_device_status(void* workspace, void* stream, int* status) {
+  return read_status_word(workspace, stream, status);
+}
+
+int mla_evict_select(int32_t batch, int32_t max_tokens, const float* weights, const int32_t* seqlens, int32_t budget,
+                     int32_t sink, int32_t recent, int32_t* kept, int32_t* kept_lens, int32_t* device_status,
+                     void* stream) {
+  CallRange range_("mla_evict_select");
+  if (batch < 1 || max_tokens < 1 || budget < 1 || sink < 0 || recent < 0) return MLA_ERR_INVALID_ARG;
+  if (int64_t(sink) + recent > budget) return MLA_ERR_INVALID_ARG;
+  if (max_tokens > (1 << 30) || budget > (1 << 30)) return MLA_ERR_UNSUPPORTED;
+  if (!weights || !seqlens || !kept || !kept_lens) return MLA_ERR_INVALID_ARG;
+  if (!aligned(weights, 4) || !aligned(seqlens, 4) || !aligned(kept, 4) || !aligned(kept_lens, 4) ||
+      !aligned(device_status, 4))
+    return MLA_ERR_INVALID_ARG;
+  return launch_evict_select(weights, max_tokens, seqlens, batch, budget, sink, recent, kept, kept_lens, device_status,
+                             static_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? MLA_OK
+             : MLA_ERR_CUDA;
+}
+
+size_t mla_compact_workspace_bytes(const mla_shape_t* shape, int max_rows) {
+  if (check_shape(shape) != MLA_OK || max_rows < 1 || max_rows > (1 << 30)) return 0;
+  return compact_workspace_bytes(shape->batch, max_rows);
+}
+
+int mla_cache_compact(const mla_shape_t* shape, void* kv_cache, float* kv_scale, const int32_t* block_table,
+                      const int32_t* src, const int32_t* src_lens, const int32_t* base, int32_t max_rows, float* weights,
+                      void* workspace, size_t workspace_bytes, void* stream) {
+  CallRange range_("mla_cache_compact");
+  const int rc = check_shape(shape);
+  if (rc != MLA_OK) return rc;
+  if (!kv_cache || !block_table || !src || !src_lens || !workspace || max_rows < 1) return MLA_ERR_INVALID_ARG;
+  if (shape->cache_dtype == MLA_CACHE_FP8_E4M3 && !kv_scale) return MLA_ERR_INVALID_ARG;
+  if (!aligned(kv_cache, 256) || !aligned(kv_scale, 4) || !aligned(block_table, 4) || !aligned(src, 4) ||
+      !aligned(src_lens, 4) || !aligned(base, 4) || !aligned(weights, 4) || !aligned(workspace, 256))
+    return MLA_ERR_INVALID_ARG;
+  const size_t need = mla_compact_workspace_bytes(shape, max_rows);
+  if (need == 0) return MLA_ERR_UNSUPPORTED;
+  if (workspace_bytes < need) return MLA_ERR_WORKSPACE;
+  return launch_compact(shape, kv_cache, kv_scale, block_table, src, src_lens, base, max_rows, weights, workspace,
+                        static_cast<cudaStream_t>(stream));
+}
+
+int mla_compact_get_device_status(void* workspace, void* stream, int* status) {
+  return read_status_word(workspace, stream, status);
 }
 
 int mla_absorb_q(int32_t rows, int32_t num_heads, const void* q, const void* w_k, void* qz, int32_t* device_status,

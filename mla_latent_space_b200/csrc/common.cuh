@@ -58,7 +58,23 @@ MLA_HD int64_t ceil_div64(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 struct ShapeInfo {
   int batch, s_q, heads, causal, max_pages, tiles_per_req;
+  // tree decode: query token i of request r is node i of its drafted tree, of
+  // which it holds draft_lens[r] (null: every slot that its length allows)
+  int tree = 0;
+  const int32_t* draft_lens = nullptr;
 };
+
+// Nodes of request r's drafted tree: the last n of its t tokens.  A count
+// outside [0, min(s_q, t)] is clamped and flagged; without counts every slot
+// holds a node, as far as the length allows.
+MLA_HD int tree_nodes(const int32_t* draft_lens, int r, int s_q, int t, int32_t* flag) {
+  const int cap = s_q < t ? s_q : t;
+  if (draft_lens == nullptr) return cap;
+  const int n = draft_lens[r];
+  if (n < 0) { *flag |= kStatusBadSeqlen; return 0; }
+  if (n > cap) { *flag |= kStatusBadSeqlen; return cap; }
+  return n;
+}
 
 // Keys visible to query token i of a request holding t cached tokens.
 MLA_HD int visible_len(int t, int s_q, int i, int causal) {
@@ -75,6 +91,13 @@ MLA_HD int tile_pages(const ShapeInfo& s, int t, int qt) {
   int i_last = (last - 1) / s.heads;
   int L = visible_len(t, s.s_q, i_last, s.causal);
   return (L + MLA_PAGE_SIZE - 1) / MLA_PAGE_SIZE;
+}
+
+// The same for tile qt of request r, whose length (clamped) is t.  Tree
+// decode: a tile whose first row belongs to no node walks nothing.
+MLA_HD int request_tile_pages(const ShapeInfo& s, int r, int t, int qt, int32_t* flag) {
+  if (s.tree && qt * MLA_TILE_ROWS / s.heads >= tree_nodes(s.draft_lens, r, s.s_q, t, flag)) return 0;
+  return tile_pages(s, t, qt);
 }
 
 MLA_HD int tile_cost(int pages) { return pages > 0 ? pages + kPieceOverhead : 0; }

@@ -11,6 +11,14 @@
 
 namespace mla {
 
+// Tree decode: the drafted trees' node counts (null: s_q, as far as the
+// length allows) and mask rows, int64 [batch, s_q, mask_words].
+struct TreeArgs {
+  const int32_t* draft_lens = nullptr;
+  const int64_t* mask = nullptr;
+  int mask_words = 0;
+};
+
 // What prepare_decode_sm100 builds: the TMA descriptors over the page pool
 // and the query rows, and the launch geometry.  Plain data, valid for the
 // pointers and shape it was built from.
@@ -22,8 +30,9 @@ struct DecodePrepared {
 
 // Host work only: encodes the tensor maps and sets the kernel's dynamic
 // shared-memory limit on the current device.  Returns MLA_OK or
-// MLA_ERR_CUDA; enqueues nothing.
-int prepare_decode_sm100(const mla_shape_t* shape, const void* q, const void* kv, DecodePrepared* pr);
+// MLA_ERR_CUDA; enqueues nothing.  tree: the launch will be a tree decode.
+int prepare_decode_sm100(const mla_shape_t* shape, const void* q, const void* kv, DecodePrepared* pr,
+                         bool tree = false);
 
 // Enqueues the decode kernel built by prepare_decode_sm100 on `stream`.
 // out_lo (optional, bf16 like out): whole tiles then write O as two terms,
@@ -31,10 +40,11 @@ int prepare_decode_sm100(const mla_shape_t* shape, const void* q, const void* kv
 // combine (launch_combine with the same out_lo).
 // test_stall: 0, except from the test library's stalled-decode entry point
 // (a bounded wait in the kernel then runs out on purpose).
+// tree: null, or the arguments of a tree decode (as prepared).
 int enqueue_decode_sm100(const DecodePrepared& pr, const mla_shape_t* shape, const void* q, const void* kv,
                          const float* kv_scale, const int32_t* block_table, const int32_t* seqlens, float scale,
                          const void* sched, void* ws, int cap_slots, void* out, float* lse, cudaStream_t stream,
-                         void* out_lo = nullptr, int test_stall = 0);
+                         void* out_lo = nullptr, int test_stall = 0, const TreeArgs* tree = nullptr);
 
 // prepare + enqueue.
 int launch_decode_sm100(const mla_shape_t* shape, const void* q, const void* kv, const float* kv_scale,

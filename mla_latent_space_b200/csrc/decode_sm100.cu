@@ -186,6 +186,7 @@ struct Params {
   int cap_slots;
   int q_rows;         // batch * s_q * heads
   int test_stall;     // test hook, 0 in every product call (see the QK issuer)
+  TreeArgs tree;      // tree decode only
 };
 
 
@@ -434,10 +435,32 @@ __device__ __forceinline__ int clamp_len(int t, const SchedView& sv) {
   return max(0, min(t, sv.max_pages * MLA_PAGE_SIZE));
 }
 
+// Tree decode: which of the 64 positions of page j a row sees, bit c for
+// position 64 j + c.  The row is that of a node whose mask words are m (W of
+// them), in a request of `prefix` committed tokens followed by n drafted
+// ones.  Bits of m past the n drafted tokens count for nothing.
+__device__ __forceinline__ uint64_t tree_visible(const int64_t* m, int W, int prefix, int n, int j) {
+  const int off = j * MLA_PAGE_SIZE - prefix;   // place of the page's first position among the drafted tokens
+  if (off + MLA_PAGE_SIZE <= 0) return ~0ull;
+  auto word = [&](int k) -> uint64_t {
+    const int left = n - 64 * k;
+    if (k >= W || left <= 0) return 0ull;
+    const uint64_t w = uint64_t(m[k]);
+    return left >= 64 ? w : w & ((1ull << left) - 1);
+  };
+  if (off < 0) return ((1ull << -off) - 1) | (word(0) << -off);
+  const int k = off >> 6, sh = off & 63;
+  return sh == 0 ? word(k) : (word(k) >> sh) | (word(k + 1) << (64 - sh));
+}
+
 // kFp8: the cache pages hold e4m3 latent values with per-token scales and a
 // bf16 RoPE part (pool_map covers the e4m3 bytes, rope_map the RoPE values);
 // otherwise pool_map covers bf16 rows and rope_map is not used.
-template <bool kFp8>
+// kTree: query token i is node i of the request's drafted tree; it sees the
+// committed prefix and the drafted tokens of its mask row (tree_visible).
+// Only the softmax differs: 64 visibility bits a page in the place of a
+// count of visible tokens, one register test a column either way.
+template <bool kFp8, bool kTree>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 decode_sm100_kernel(const __grid_constant__ CUtensorMap pool_map, const __grid_constant__ CUtensorMap q_map,
                     const __grid_constant__ CUtensorMap rope_map, const Params p) {
@@ -769,7 +792,17 @@ decode_sm100_kernel(const __grid_constant__ CUtensorMap pool_map, const __grid_c
         const int rho = qt * MLA_TILE_ROWS + i;
         const bool valid = rho < rows_total;
         const int t = clamp_len(p.seqlens[r], sv);
-        const int Lrow = valid ? visible_len(t, sv.s_q, rho / sv.heads, sv.causal) : 0;
+        int Lrow = valid ? visible_len(t, sv.s_q, rho / sv.heads, sv.causal) : 0;
+        int prefix = 0, nodes = 0;   // tree decode: committed and drafted tokens
+        const int64_t* mrow = nullptr;
+        if constexpr (kTree) {
+          int32_t flag = 0;   // the scheduler flagged a count out of range
+          nodes = tree_nodes(p.tree.draft_lens, r, sv.s_q, t, &flag);
+          prefix = t - nodes;
+          const int node = rho / sv.heads;
+          if (node >= nodes) Lrow = 0;
+          mrow = p.tree.mask + (size_t(r) * sv.s_q + min(node, sv.s_q - 1)) * p.tree.mask_words;
+        }
         // query row i -> TMEM lane i.  Box c of the query (rows 0-63, then
         // 64-127 at +8 KB) is sub-stage c % qbs of stage zc + c / qbs.  BF16
         // cache: boxes 0-8, two per stage, as bf16 pairs in columns [0, 288),
@@ -856,6 +889,12 @@ decode_sm100_kernel(const __grid_constant__ CUtensorMap pool_map, const __grid_c
             if (page >= 0 && page < p.num_pages) nv = Lrow - jp * MLA_PAGE_SIZE;
             else page = -1;
           }
+          uint32_t vis_lo = 0u, vis_hi = 0u;
+          if constexpr (kTree) {
+            const uint64_t vis = nv > 0 ? tree_visible(mrow, p.tree.mask_words, prefix, nodes, jp) : 0ull;
+            vis_lo = uint32_t(vis);
+            vis_hi = uint32_t(vis >> 32);
+          }
           if constexpr (kFp8) {
             // the page's per-token scales, published by the barrier below
             if (i < 64) st_shared_u32(scl + 4u * uint32_t(i), __float_as_uint(page >= 0 ? p.kv_scale[size_t(page) * 64 + i] : 0.f));
@@ -907,8 +946,10 @@ decode_sm100_kernel(const __grid_constant__ CUtensorMap pool_map, const __grid_c
           float mh = -INFINITY;
 #pragma unroll
           for (int c = 0; c < 32; ++c) {
-            x[c] = c < nv ? x[c] * p.scale_log2 : -INFINITY;
-            x[c + 32] = c + 32 < nv ? x[c + 32] * p.scale_log2 : -INFINITY;
+            const bool see0 = kTree ? ((vis_lo >> c) & 1u) != 0 : c < nv;
+            const bool see1 = kTree ? ((vis_hi >> c) & 1u) != 0 : c + 32 < nv;
+            x[c] = see0 ? x[c] * p.scale_log2 : -INFINITY;
+            x[c + 32] = see1 ? x[c + 32] * p.scale_log2 : -INFINITY;
             mh = fmaxf(mh, fmaxf(x[c], x[c + 32]));
           }
           asm volatile("st.shared.f32 [%0], %1;" ::"r"(xmax + 4u * uint32_t(g)), "f"(mh) : "memory");
@@ -1378,10 +1419,16 @@ bool make_q_map(CUtensorMap* map, const void* q, int rows) {
   return r == CUDA_SUCCESS;
 }
 
+using DecodeKernel = void (*)(const CUtensorMap, const CUtensorMap, const CUtensorMap, const Params);
+DecodeKernel decode_kernel(bool fp8, bool tree) {
+  if (tree) return fp8 ? &decode_sm100_kernel<true, true> : &decode_sm100_kernel<false, true>;
+  return fp8 ? &decode_sm100_kernel<true, false> : &decode_sm100_kernel<false, false>;
+}
+
 }  // namespace
 
 
-int prepare_decode_sm100(const mla_shape_t* shape, const void* q, const void* kv, DecodePrepared* pr) {
+int prepare_decode_sm100(const mla_shape_t* shape, const void* q, const void* kv, DecodePrepared* pr, bool tree) {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return MLA_ERR_CUDA;
   if (cudaDeviceGetAttribute(&pr->sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || pr->sms <= 0)
@@ -1395,9 +1442,7 @@ int prepare_decode_sm100(const mla_shape_t* shape, const void* q, const void* kv
     pr->rope_map = pr->pool_map;   // not read
   }
   if (!make_q_map(&pr->q_map, q, q_rows)) return MLA_ERR_CUDA;
-  if (!ensure_smem_attr(reinterpret_cast<const void*>(pr->fp8 ? &decode_sm100_kernel<true>
-                                                               : &decode_sm100_kernel<false>),
-                        int(kSmemBytes)))
+  if (!ensure_smem_attr(reinterpret_cast<const void*>(decode_kernel(pr->fp8, tree)), int(kSmemBytes)))
     return MLA_ERR_CUDA;
   return MLA_OK;
 }
@@ -1405,7 +1450,7 @@ int prepare_decode_sm100(const mla_shape_t* shape, const void* q, const void* kv
 int enqueue_decode_sm100(const DecodePrepared& pr, const mla_shape_t* shape, const void* q, const void* kv,
                          const float* kv_scale, const int32_t* block_table, const int32_t* seqlens, float scale,
                          const void* sched, void* ws, int cap_slots, void* out, float* lse, cudaStream_t stream,
-                         void* out_lo, int test_stall) {
+                         void* out_lo, int test_stall, const TreeArgs* tree) {
   Params prm;
   prm.q = static_cast<const uint16_t*>(q);
   prm.kv = static_cast<const uint8_t*>(kv);
@@ -1422,6 +1467,7 @@ int enqueue_decode_sm100(const DecodePrepared& pr, const mla_shape_t* shape, con
   prm.cap_slots = cap_slots;
   prm.q_rows = shape->batch * shape->s_q * shape->num_heads;
   prm.test_stall = test_stall;
+  prm.tree = tree != nullptr ? *tree : TreeArgs{};
   const int clusters = pr.sms / 2 > 0 ? pr.sms / 2 : 1;
   // programmatic dependent launch: the prologue (barriers, TMEM, descriptor
   // prefetch) overlaps the scheduler kernel; the kernel waits for it before
@@ -1436,9 +1482,8 @@ int enqueue_decode_sm100(const DecodePrepared& pr, const mla_shape_t* shape, con
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  const cudaError_t e =
-      pr.fp8 ? cudaLaunchKernelEx(&cfg, decode_sm100_kernel<true>, pr.pool_map, pr.q_map, pr.rope_map, prm)
-             : cudaLaunchKernelEx(&cfg, decode_sm100_kernel<false>, pr.pool_map, pr.q_map, pr.rope_map, prm);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, decode_kernel(pr.fp8, tree != nullptr), pr.pool_map, pr.q_map,
+                                           pr.rope_map, prm);
   return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
 }
 

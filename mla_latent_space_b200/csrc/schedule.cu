@@ -171,7 +171,7 @@ schedule_kernel(const int32_t* __restrict__ seqlens, ShapeInfo s, int W, int32_t
   for (int T = t0; T < t1; ++T) {
     const int r = T / s.tiles_per_req, qt = T % s.tiles_per_req;
     const int t = clamp_seqlen(seqlens[r], s.max_pages, &flag);
-    const int pages = tile_pages(s, t, qt);
+    const int pages = request_tile_pages(s, r, t, qt, &flag);
     pages_sm[T] = pages;
     local += tile_cost(pages);
   }
@@ -285,7 +285,7 @@ MLA_HD void plan_schedule_seq(const int32_t* seqlens, const ShapeInfo& s, int W,
   for (int T = 0; T < num_tiles; ++T) {
     int r = T / s.tiles_per_req, qt = T % s.tiles_per_req;
     int t = clamp_seqlen(seqlens[r], s.max_pages, &flag);
-    int pages = tile_pages(s, t, qt);
+    int pages = request_tile_pages(s, r, t, qt, &flag);
     tiles[size_t(T) * kTileInts + T_PAGES] = pages;
     tiles[size_t(T) * kTileInts + T_PREFIX] = int32_t(total);
     total += tile_cost(pages);

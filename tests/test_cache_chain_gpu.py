@@ -1,0 +1,99 @@
+"""The tree decode, the acceptance, the attention weights, the eviction and
+the compaction in a row, as a serving loop runs them, on the GPU against the
+fp64 oracle.
+"""
+import numpy as np
+import pytest
+import torch
+
+import mla_latent_space_b200 as mla
+import mla_workloads as mw
+import oracle
+from gpu_helpers import assert_parity, compare
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    from mla_latent_space_b200 import build
+    build.build()
+    assert torch.cuda.is_available()
+
+
+@pytest.mark.parametrize("cache", ["bf16", "fp8"])
+def test_draft_verify_accept_weigh_evict_decode(cache):
+    b, h, s = 3, 128, 8
+    wl = mw.make(b, s, h, [500, 77, 1300], seed=100, cache_dtype=cache, name="chain")
+    par = np.array([[-1, 0, 0, 1, 1, 2, 3, 3], [-1, -1, 0, 1, 2, 2, 4, 5], [-1, 0, 1, 2, 3, 4, 5, 6]], dtype=np.int32)
+    bt, sl = torch.from_numpy(wl.block_table).cuda(), torch.from_numpy(wl.seqlens).cuda()
+    pool, sc = wl.pool.cuda(), None if wl.kv_scale is None else wl.kv_scale.cuda()
+    q = wl.q.cuda()
+
+    # verify the tree
+    tree = mla.TreeDecoder(mla.make_shape(b, s, h, wl.max_pages, wl.num_pages, cache))
+    mask = torch.empty((b, s, 1), dtype=torch.int64, device="cuda")
+    out = torch.empty((b, s, h, 512), dtype=torch.bfloat16, device="cuda")
+    lse = torch.empty((b, s, h), dtype=torch.float32, device="cuda")
+    mla.mla_tree_mask(torch.from_numpy(par).cuda(), mask)
+    tree.decode(q, pool, bt, sl, mask, wl.softmax_scale, out, lse, kv_scale=sc)
+    O_ref, L_ref = oracle.tree_decode(wl, oracle.tree_mask(par))
+    assert_parity(compare(out.float().cpu().numpy(), lse.cpu().numpy(), O_ref, L_ref), "tree")
+    assert tree.status() == 0
+
+    # accept one path of each: it closes up behind the prefix
+    paths = [[0, 1, 3, 7], [1, 3], [0, 1, 2, 3, 4, 5, 6, 7]]
+    base = wl.seqlens - s
+    src, n = np.full((b, s), -1, dtype=np.int32), np.array([len(p) for p in paths], dtype=np.int32)
+    for r, p in enumerate(paths):
+        src[r, :len(p)] = base[r] + np.array(p)
+    shape1 = mla.make_shape(b, 1, h, wl.max_pages, wl.num_pages, cache)
+    accept = mla.CacheCompactor(shape1, s)
+    accept.compact(pool, bt, torch.from_numpy(src).cuda(), torch.from_numpy(n).cuda(),
+                   base=torch.from_numpy(base.astype(np.int32)).cuda(), kv_scale=sc)
+    assert accept.status() == 0
+    wl.pool, wl.kv_scale, _ = oracle.compact(wl.pool, wl.kv_scale, wl.block_table, src, n, base)
+    wl.seqlens = (base + n).astype(np.int32)
+    sl.copy_(torch.from_numpy(wl.seqlens))
+
+    # the next token decodes over the closed-up cache and leaves its weights
+    wl.q, wl.s_q = wl.q[:, :1].contiguous(), 1
+    q1 = wl.q.cuda()
+    dec = mla.Decoder(shape1)
+    out1 = torch.empty((b, 1, h, 512), dtype=torch.bfloat16, device="cuda")
+    lse1 = torch.empty((b, 1, h), dtype=torch.float32, device="cuda")
+    dec.schedule(sl)
+    dec.decode(q1, pool, sc, bt, sl, wl.softmax_scale, out1, lse1)
+    O_ref, L_ref = oracle.decode(wl)
+    assert_parity(compare(out1.float().cpu().numpy(), lse1.cpu().numpy(), O_ref, L_ref), "accepted")
+    w = torch.zeros((b, wl.max_pages * 64), device="cuda")
+    acc = mla.AttnWeights(shape1)
+    acc.accumulate(q1, pool, bt, sl, lse1, wl.softmax_scale, 1.0, w, kv_scale=sc)
+    got = w.cpu().numpy().astype(np.float64)
+    ref = oracle.attn_weights(wl, L_ref, 0.0, np.zeros_like(got))
+    # 5e-4 of a weight from its own arithmetic (see the weights' tests), 1e-3 from the decode's lse
+    assert (np.abs(got - ref) <= 1.5e-3 * ref).all()
+
+    # cut every request to its budget: the kept list is the sparse decode's list
+    budget = 64
+    kept = torch.empty((b, budget), dtype=torch.int32, device="cuda")
+    n_kept = torch.empty(b, dtype=torch.int32, device="cuda")
+    mla.mla_evict_select(w, sl, budget, 4, 8, kept, n_kept)
+    k_ref, n_ref = oracle.evict_select(w.cpu().numpy(), wl.seqlens, budget, 4, 8)
+    assert np.array_equal(kept.cpu().numpy(), k_ref) and np.array_equal(n_kept.cpu().numpy(), n_ref)
+    sparse = mla.SparseDecoder(shape1, budget)
+    out_s, lse_s = torch.empty_like(out1), torch.empty_like(lse1)
+    sparse.decode(q1, pool, bt, sl, kept.view(b, 1, budget), wl.softmax_scale, out_s, lse_s, kv_scale=sc)
+
+    # close up and decode again: the same rows, now dense
+    comp = mla.CacheCompactor(shape1, budget)
+    comp.compact(pool, bt, kept, n_kept, kv_scale=sc, weights=w)
+    assert comp.status() == 0
+    dec.schedule(n_kept)
+    dec.decode(q1, pool, sc, bt, n_kept, wl.softmax_scale, out1, lse1)
+    wl.pool, wl.kv_scale, w_ref = oracle.compact(wl.pool, wl.kv_scale, wl.block_table, k_ref, n_ref, None, got.astype(np.float32))
+    wl.seqlens = n_ref
+    O_ref, L_ref = oracle.decode(wl)
+    assert_parity(compare(out1.float().cpu().numpy(), lse1.cpu().numpy(), O_ref, L_ref), "dense after eviction")
+    assert_parity(compare(out_s.float().cpu().numpy(), lse_s.cpu().numpy(), O_ref, L_ref), "sparse before eviction")
+    assert np.array_equal(w.cpu().numpy(), w_ref)
