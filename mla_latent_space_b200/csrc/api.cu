@@ -43,10 +43,10 @@ size_t attn_weights_workspace_bytes(const mla_shape_t* shape, int num_sms);
 int launch_attn_weights(const mla_shape_t* shape, const void* q, const void* kv, const float* kv_scale,
                         const int32_t* block_table, const int32_t* seqlens, const float* lse, float scale, float decay,
                         float* weights, void* ws, int num_sms, cudaStream_t stream);
-cudaError_t launch_evict_select(const float* weights, int64_t max_tokens, const int32_t* seqlens, int batch, int budget,
+cudaError_t launch_evict_select(const float* weights, int max_tokens, const int32_t* seqlens, int batch, int budget,
                                 int sink, int recent, int32_t* kept, int32_t* kept_lens, int32_t* status,
                                 cudaStream_t stream);
-size_t compact_workspace_bytes(int batch, int max_rows);
+size_t compact_workspace_bytes(const mla_shape_t* shape, int max_rows);
 int launch_compact(const mla_shape_t* shape, void* kv, float* kv_scale, const int32_t* block_table, const int32_t* src,
                    const int32_t* src_lens, const int32_t* base, int max_rows, float* weights, void* ws,
                    cudaStream_t stream);
@@ -610,7 +610,7 @@ int mla_evict_select(int32_t batch, int32_t max_tokens, const float* weights, co
 
 size_t mla_compact_workspace_bytes(const mla_shape_t* shape, int max_rows) {
   if (check_shape(shape) != MLA_OK || max_rows < 1 || max_rows > (1 << 30)) return 0;
-  return compact_workspace_bytes(shape->batch, max_rows);
+  return compact_workspace_bytes(shape, max_rows);
 }
 
 int mla_cache_compact(const mla_shape_t* shape, void* kv_cache, float* kv_scale, const int32_t* block_table,

@@ -3,18 +3,47 @@
 // `sink`, the last `recent` and, between them, the budget - sink - recent of
 // the largest weight stay; of equal weights the lowest positions.
 //
-// One CTA per request: a radix select (8 bits a pass, histogram in shared
-// memory) finds the threshold weight and how many tokens of exactly that
-// weight stay, then one ordered pass writes the kept positions.
+// Mathematics.  Every token gets an unsigned 32-bit key in the order of the
+// weights (NaN 0, sink and recent tokens the largest key, which no weight
+// has); what stays are the `budget` largest keys, ties by position.  A radix
+// select finds the smallest kept key `thr` in at most three passes of 11, 11
+// and 10 bits (a histogram of the keys that match the digits so far, the
+// suffix sum that reaches what is still needed), and stops early when a
+// bucket is needed whole.  One ordered pass then writes the positions with
+// key > thr and the first `need` of those with key == thr.
+//
+// Layout.  The weights are read once: the keys stay in shared memory.  A row
+// of up to kWideTokens tokens is one CTA's work; a longer one is cut into
+// contiguous chunks over a cluster of 8 CTAs, which add up each other's
+// histograms and counts over distributed shared memory.  Rows too long even
+// for that re-read the weights through L2 in every pass.  What bounds it is
+// latency: a launch, one trip to memory, and five block- or cluster-wide
+// barriers.
+#include <cooperative_groups.h>
 #include <cuda_runtime.h>
 
 #include "kernel_util.cuh"
+
+namespace cg = cooperative_groups;
 
 namespace mla {
 
 namespace {
 
 constexpr int kSelThreads = 1024;
+constexpr int kSelWarps = kSelThreads / 32;
+constexpr int kBins = 2048;
+constexpr int kPasses = 3;
+constexpr int kCluster = 8;
+constexpr int kWideTokens = 8192;
+constexpr int kSmemKeys = 48 * 1024;         // keys per CTA that fit beside the histograms (192 KB)
+
+struct alignas(16) SelShared {
+  int hist[kPasses][kBins];
+  int warp_a[kSelWarps], warp_b[kSelWarps];
+  int digit, need, count;                    // a pass's verdict
+  int cta_gt, cta_eq;                        // this CTA's chunk: keys above thr, keys equal to it
+};
 
 // Unsigned key in the order of the weights; NaN below everything, -0 = +0.
 __device__ __forceinline__ uint32_t weight_key(float w) {
@@ -23,98 +52,214 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
   return (b & 0x80000000u) ? ~b : b | 0x80000000u;
 }
 
-// Exclusive block-wide scan of one value a thread; *total gets the sum.
-__device__ int block_scan(int v, int* warp_sums, int* total) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int inc = v;
-#pragma unroll
-  for (int off = 1; off < 32; off <<= 1) {
-    const int u = __shfl_up_sync(0xffffffffu, inc, off);
-    if (lane >= off) inc += u;
-  }
-  __syncthreads();
-  if (lane == 31) warp_sums[warp] = inc;
-  __syncthreads();
-  int base = 0, sum = 0;
-  for (int k = 0; k < kSelThreads / 32; ++k) {
-    base += k < warp ? warp_sums[k] : 0;
-    sum += warp_sums[k];
-  }
-  *total = sum;
-  return base + inc - v;
+// hist[bin] += 1 for every lane with `in`.  The first such lane's bin is
+// added once for all lanes that share it: many weights are equal (zeros), and
+// 32 adds to one address would queue.
+__device__ __forceinline__ void count_bin(int* hist, bool in, int bin, int lane) {
+  const unsigned live = __ballot_sync(0xffffffffu, in);
+  if (live == 0) return;
+  const int first = __ffs(int(live)) - 1;
+  const int lead = __shfl_sync(0xffffffffu, bin, first);
+  const unsigned same = __ballot_sync(0xffffffffu, in && bin == lead);
+  if (lane == first) atomicAdd(&hist[lead], __popc(same));
+  else if (in && bin != lead) atomicAdd(&hist[bin], 1);
 }
 
+// Sum of v over the CTA's warps before this one, exclusive; all threads call.
+__device__ __forceinline__ int warp_prefix(const int* sums, int warp, int lane) {
+  int v = lane < warp ? sums[lane] : 0;
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+  return v;
+}
+
+template <int kCtas, bool kInSmem>
 __global__ void __launch_bounds__(kSelThreads)
-evict_select_kernel(const float* __restrict__ weights, int64_t max_tokens, const int32_t* __restrict__ seqlens, int budget,
+evict_select_kernel(const float* __restrict__ weights, int max_tokens, const int32_t* __restrict__ seqlens, int budget,
                     int sink, int recent, int32_t* __restrict__ kept, int32_t* __restrict__ kept_lens,
                     int32_t* __restrict__ status) {
-  __shared__ int hist[256];
-  __shared__ int warp_sums[kSelThreads / 32];
-  __shared__ uint32_t prefix_sh;
-  __shared__ int need_sh;
-  const int r = blockIdx.x, tid = threadIdx.x;
-  int64_t t64 = seqlens[r];
-  if (t64 < 0 || t64 > max_tokens) {
-    if (tid == 0 && status != nullptr) atomicOr(status, kStatusBadSeqlen);
-    t64 = t64 < 0 ? 0 : max_tokens;
+  extern __shared__ uint32_t keys[];
+  __shared__ SelShared sh;
+  const int r = blockIdx.x / kCtas, rank = blockIdx.x % kCtas;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  int t = seqlens[r];
+  if (t < 0 || t > max_tokens) {
+    if (rank == 0 && tid == 0 && status != nullptr) atomicOr(status, kStatusBadSeqlen);
+    t = t < 0 ? 0 : max_tokens;
   }
-  const int t = int(t64);
   const float* w = weights + size_t(r) * size_t(max_tokens);
   int32_t* out = kept + size_t(r) * size_t(budget);
-  if (tid == 0) kept_lens[r] = min(t, budget);
-  if (t <= budget) {
-    for (int k = tid; k < budget; k += kSelThreads) out[k] = k < t ? k : -1;
+  if (rank == 0 && tid == 0) kept_lens[r] = min(t, budget);
+  if (t <= budget) {   // (every CTA of the cluster agrees)
+    for (int k = rank * kSelThreads + tid; k < budget; k += kCtas * kSelThreads) out[k] = k < t ? k : -1;
     return;
   }
-  const int lo = sink, hi = t - recent;
-  int need = budget - sink - recent;   // of the tokens in [lo, hi)
+  for (int k = tid; k < kPasses * kBins; k += kSelThreads) (&sh.hist[0][0])[k] = 0;
+  __syncthreads();
+
+  // this CTA's chunk [lo, lo + n), a multiple of 32 tokens but for the last
+  const int chunk = ((t + kCtas - 1) / kCtas + 31) & ~31;
+  const int lo = min(t, rank * chunk), n = min(t - lo, chunk);
+  const int n32 = (n + 31) & ~31;
+  auto make_key = [&](int i) -> uint32_t {
+    const int j = lo + i;
+    return j < sink || j >= t - recent ? 0xffffffffu : weight_key(w[j]);
+  };
+  auto key_at = [&](int i) -> uint32_t { return kInSmem ? keys[i] : make_key(i); };
+
   uint32_t prefix = 0;
-  for (int shift = 24; need > 0 && shift >= 0; shift -= 8) {
-    for (int k = tid; k < 256; k += kSelThreads) hist[k] = 0;
+  int need = budget, shift = 21;
+  uint32_t thr = 0;
+  for (int pass = 0; pass < kPasses; ++pass) {
+    const int bits = pass < 2 ? 11 : 10;
+    const uint32_t fixed = pass == 0 ? 0u : 0xffffffffu << (shift + bits);
+    int* hist = sh.hist[pass];
+    if (pass == 0) {
+      // the only pass over memory: eight loads in flight a thread
+      constexpr int kU = 8;
+      for (int i0 = tid; i0 < n32; i0 += kU * kSelThreads) {
+        uint32_t k[kU];
+#pragma unroll
+        for (int u = 0; u < kU; ++u) {
+          const int i = i0 + u * kSelThreads;
+          k[u] = i < n ? make_key(i) : 0u;
+        }
+#pragma unroll
+        for (int u = 0; u < kU; ++u) {
+          const int i = i0 + u * kSelThreads;
+          if (i - lane >= n32) break;   // uniform in the warp
+          if (kInSmem && i < n) keys[i] = k[u];
+          count_bin(hist, i < n, int(k[u] >> 21), lane);
+        }
+      }
+    } else {
+      for (int i = tid; i < n32; i += kSelThreads) {
+        const uint32_t k = i < n ? key_at(i) : 0u;
+        count_bin(hist, i < n && (k & fixed) == prefix, int((k >> shift) & ((1u << bits) - 1u)), lane);
+      }
+    }
+    if constexpr (kCtas > 1) cg::this_cluster().sync();
+    else __syncthreads();
+    // thread tid owns bins 2046 - 2 tid and 2047 - 2 tid: its prefix over
+    // the threads before it counts the keys of all larger bins
+    int hi_bin = 0, lo_bin = 0;
+    if constexpr (kCtas > 1) {
+#pragma unroll
+      for (int c = 0; c < kCtas; ++c) {
+        const int2 v = *reinterpret_cast<const int2*>(cg::this_cluster().map_shared_rank(hist, c) + kBins - 2 - 2 * tid);
+        lo_bin += v.x;
+        hi_bin += v.y;
+      }
+    } else {
+      const int2 v = *reinterpret_cast<const int2*>(hist + kBins - 2 - 2 * tid);
+      lo_bin = v.x;
+      hi_bin = v.y;
+    }
+    int inc = lo_bin + hi_bin;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int u = __shfl_up_sync(0xffffffffu, inc, off);
+      if (lane >= off) inc += u;
+    }
+    if (lane == 31) sh.warp_a[warp] = inc;
     __syncthreads();
-    const uint32_t above = shift == 24 ? 0u : 0xffffffffu << (shift + 8);
-    for (int j = lo + tid; j < hi; j += kSelThreads) {
-      const uint32_t k = weight_key(w[j]);
-      if ((k & above) == prefix) atomicAdd(&hist[(k >> shift) & 255], 1);
+    const int above = warp_prefix(sh.warp_a, warp, lane) + inc - lo_bin - hi_bin;   // keys in larger bins
+    if (above < need && need <= above + hi_bin + lo_bin) {
+      const bool in_hi = need <= above + hi_bin;
+      sh.digit = in_hi ? kBins - 1 - 2 * tid : kBins - 2 - 2 * tid;
+      sh.need = in_hi ? need - above : need - above - hi_bin;
+      sh.count = in_hi ? hi_bin : lo_bin;
     }
     __syncthreads();
-    if (tid == 0) {
-      int b = 255, n = need;
-      while (b > 0 && hist[b] < n) n -= hist[b--];
-      prefix_sh = prefix | (uint32_t(b) << shift);
-      need_sh = n;
+    prefix |= uint32_t(sh.digit) << shift;
+    need = sh.need;
+    thr = prefix;
+    if (need == sh.count) {   // the whole bucket stays (never the bucket of key 0: fewer stay than there are)
+      thr = prefix - 1u;
+      need = 0;
+      break;
     }
-    __syncthreads();
-    prefix = prefix_sh;
-    need = need_sh;
-    __syncthreads();
+    shift -= pass == 0 ? 11 : 10;
   }
-  const bool none = budget - sink - recent == 0;
-  // keys above `prefix` stay, and the first `need` of those equal to it
-  int done = 0, eq_done = 0;
-  for (int j0 = 0; j0 < t; j0 += kSelThreads) {
-    const int j = j0 + tid;
-    const bool in = j < t, mid = in && j >= lo && j < hi;
-    const uint32_t k = mid ? weight_key(w[j]) : 0u;
-    const bool eq = mid && !none && k == prefix;
-    int eq_total, total;
-    const int eq_rank = eq_done + block_scan(eq ? 1 : 0, warp_sums, &eq_total);
-    const bool keep = in && (!mid || (!none && (k > prefix || (eq && eq_rank < need))));
-    const int at = done + block_scan(keep ? 1 : 0, warp_sums, &total);
-    if (keep) out[at] = j;
-    done += total;
-    eq_done += eq_total;
+
+  // ordered output: warp `warp` owns a contiguous run of the chunk
+  const int run = (n32 / 32 + kSelWarps - 1) / kSelWarps * 32;
+  const int b = min(n32, warp * run), e = min(n32, b + run);
+  int gt = 0, eq = 0;
+  for (int i = b + lane; i < e; i += 32) {
+    const uint32_t k = i < n ? key_at(i) : 0u;
+    gt += __popc(__ballot_sync(0xffffffffu, i < n && k > thr));
+    eq += __popc(__ballot_sync(0xffffffffu, i < n && k == thr));
   }
+  if (lane == 0) {
+    sh.warp_a[warp] = gt;
+    sh.warp_b[warp] = eq;
+  }
+  __syncthreads();
+  const int gt_before = warp_prefix(sh.warp_a, warp, lane), eq_before = warp_prefix(sh.warp_b, warp, lane);
+  int at = gt_before, eq_rank = eq_before;
+  if constexpr (kCtas > 1) {
+    if (tid == kSelThreads - 1) {
+      sh.cta_gt = gt_before + gt;
+      sh.cta_eq = eq_before + eq;
+    }
+    cg::this_cluster().sync();
+#pragma unroll
+    for (int c = 0; c < kCtas; ++c) {
+      if (c >= rank) break;
+      at += *cg::this_cluster().map_shared_rank(&sh.cta_gt, c);
+      eq_rank += *cg::this_cluster().map_shared_rank(&sh.cta_eq, c);
+    }
+  }
+  at += min(eq_rank, need);
+  const unsigned below = (1u << lane) - 1u;
+  for (int i = b + lane; i < e; i += 32) {
+    const uint32_t k = i < n ? key_at(i) : 0u;
+    const bool is_eq = i < n && k == thr;
+    const unsigned eqs = __ballot_sync(0xffffffffu, is_eq);
+    const bool keep = (i < n && k > thr) || (is_eq && eq_rank + __popc(eqs & below) < need);
+    const unsigned keeps = __ballot_sync(0xffffffffu, keep);
+    if (keep) out[at + __popc(keeps & below)] = lo + i;
+    at += __popc(keeps);
+    eq_rank += __popc(eqs);
+  }
+  if constexpr (kCtas > 1) cg::this_cluster().sync();   // no CTA leaves while another reads its counts
+}
+
+template <int kCtas, bool kInSmem>
+cudaError_t launch(const float* weights, int max_tokens, const int32_t* seqlens, int batch, int budget, int sink, int recent,
+                   int32_t* kept, int32_t* kept_lens, int32_t* status, cudaStream_t stream) {
+  auto fn = &evict_select_kernel<kCtas, kInSmem>;
+  const int chunk = ((max_tokens + kCtas - 1) / kCtas + 31) & ~31;
+  const size_t smem = kInSmem ? size_t(chunk) * 4 : 0;
+  if (!ensure_smem_attr(reinterpret_cast<const void*>(fn), kInSmem ? (kCtas > 1 ? kSmemKeys : kWideTokens) * 4 : 0))
+    return cudaErrorInvalidValue;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(unsigned(batch) * kCtas);
+  cfg.blockDim = dim3(kSelThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = kCtas;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, fn, weights, max_tokens, seqlens, budget, sink, recent, kept, kept_lens,
+                                           status);
+  return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 }  // namespace
 
-cudaError_t launch_evict_select(const float* weights, int64_t max_tokens, const int32_t* seqlens, int batch, int budget,
+cudaError_t launch_evict_select(const float* weights, int max_tokens, const int32_t* seqlens, int batch, int budget,
                                 int sink, int recent, int32_t* kept, int32_t* kept_lens, int32_t* status,
                                 cudaStream_t stream) {
-  evict_select_kernel<<<unsigned(batch), kSelThreads, 0, stream>>>(weights, max_tokens, seqlens, budget, sink, recent, kept,
-                                                                    kept_lens, status);
-  return cudaGetLastError();
+  const auto fn = max_tokens <= kWideTokens              ? &launch<1, true>
+                  : max_tokens <= kCluster * kSmemKeys ? &launch<kCluster, true>
+                                                         : &launch<kCluster, false>;
+  return fn(weights, max_tokens, seqlens, batch, budget, sink, recent, kept, kept_lens, status, stream);
 }
 
 }  // namespace mla
