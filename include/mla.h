@@ -333,7 +333,7 @@ int mla_tree_mask(int32_t batch, int32_t s_q, const int32_t* parents, const int3
  *             bytes, 256-byte aligned, zero-filled before its first use (it
  *             holds the status word); the caller must not touch it while the
  *             call's work runs, and calls that may overlap in time need one
- *             each.
+ *             each.  After MLA_ERR_TIMEOUT it must be zero-filled anew.
  * Tokens of a page whose id is out of range receive nothing (flagged). */
 size_t mla_attn_weights_workspace_bytes(const mla_shape_t* shape, int num_sms);
 int mla_attn_weights_fwd(const mla_shape_t* shape, const void* q, const void* kv_cache, const float* kv_scale,

@@ -3,111 +3,697 @@
 //             exp(scale * q_{i,h} . C_j - lse_{i,h})
 // with the lse that the decode returned.
 //
-// One CTA per (page, request): the page's 64 rows sit in shared memory as
-// fp32, the query rows pass through in groups, and every thread holds one
-// token's scores against a quarter of a group.
-#include <cuda_runtime.h>
+// Why tokens are the rows of the product.  The sum runs over query rows, so
+// S^T = C . Q^T puts a token on a TMEM lane and the rows on its columns: the
+// thread that owns the lane adds up exp2(S^T * scale' - lse') over its columns
+// in registers, and nothing is exchanged or normalised (the lse is known).
+//
+// Why a CTA pair.  One MMA covers 256 tokens x up to 256 rows over the two
+// SMs of a cluster (cta_group::2): each SM holds its 128 tokens and half of
+// the rows, so a tile of rows costs each SM's shared memory half of what it
+// would alone (9 chunks x 128 rows x 128 bytes = 144 KB for 256 rows) and a
+// page is loaded once per 256 rows.  The rows of a tile stay in shared memory
+// while the pair's tokens pass through a ring of 16 KB stages (one 128-byte
+// column box of 128 tokens each), as deep as the rows leave room for.
+//
+// Roles (both CTAs; 256 threads): warp 0 streams pages and rows by TMA,
+// signalling the pair's first CTA; warp 1 of the first CTA issues the MMAs
+// into one of two TMEM accumulators; warps 4-7 drain the other one: one
+// fused multiply-add, one exp2 and one add a score.
+//
+// Split.  The work is (request, 256-token unit, tile of rows).  Every pair
+// counts the units from the lengths and takes an equal share, in the order
+// (request, group of tiles, unit).  With enough units to fill the machine
+// the tiles form one group and a unit's weights stay with one thread; with
+// fewer than 4 a pair, the tiles are cut into up to 16 groups whose sums go
+// through the workspace, and the last group to finish a unit adds them in
+// their order: no order of sums depends on timing.
+//
+// FP8 cache: the e4m3 bytes go to the tensor core as they are (kind::f8f6f4)
+// against a two-part e4m3 copy of the query (hi + lo with a power-of-two
+// scale per row, which reproduces bf16), made by a small kernel before; the
+// RoPE columns are a bf16 product with an accumulator of its own, since the
+// token's scale multiplies the latent part alone.
+//
+// Every wait is bounded: a wait that runs out sets a status bit, both CTAs
+// leave their loops, the copies in flight are given time to land, and TMEM
+// is freed.
+#include <cuda.h>
 
+#include "decode_launch.cuh"
 #include "kernel_util.cuh"
+#include "sm100_ptx.cuh"
 
 namespace mla {
 
 namespace {
 
+using namespace ptx;
+
 constexpr int kWThreads = 256;
-constexpr int kWGroup = 16;                     // query rows per pass
-constexpr int kWRow = MLA_D_QK + 1;             // padded row of floats
-constexpr size_t kWSmem = sizeof(float) * (size_t(MLA_PAGE_SIZE) * kWRow + size_t(kWGroup) * MLA_D_QK + 4 * MLA_PAGE_SIZE);
+constexpr int kUnit = 256;                       // tokens of a unit: 128 on each CTA
+constexpr int kHalf = kUnit / 2;
+constexpr uint32_t kWBox = 8192;                 // 64 tokens x 128 bytes
+constexpr uint32_t kWStage = 2 * kWBox;
+constexpr int kWMaxStages = 12;
+constexpr uint32_t kWHead = 3072;                // barriers and column constants
+constexpr uint32_t kWSmem = 232448;
+constexpr int kMaxGroups = 16;                   // groups of row tiles per unit
+constexpr int kSplitBelow = 4;                   // units a pair below which the tiles are grouped
+constexpr uint64_t kWTimeoutNs = 2000000000ull;
+constexpr uint32_t kEpiBar = 1;
+
+// One stage per 128 bytes of a token's row.  BF16: 9 of 64 columns.  FP8: the
+// RoPE columns, then 4 of 128 e4m3 bytes, each against a hi and a lo chunk.
+template <bool kFp8>
+struct W {
+  static constexpr int stages = kFp8 ? 5 : 9;    // of a unit
+  static constexpr int tile = kFp8 ? 128 : 256;  // most rows of a tile (FP8: two accumulators a buffer)
+};
+
+struct WBars {
+  uint64_t full[kWMaxStages], empty[kWMaxStages], q_full[9], q_free[9], d_full[2], d_empty[2], done;
+  uint32_t tmem_base;
+  int32_t abort;
+  int32_t r0, base0, total, warp_sum[kWThreads / 32];
+  int32_t last;          // the epilogue's verdict: this CTA finished the unit
+};
+constexpr uint32_t kOffNlse = 512, kOffVis = 1536, kOffGmin = 2560, kOffGmax = 2592;
+static_assert(sizeof(WBars) <= kOffNlse, "barriers");
 
 struct WArgs {
-  const uint16_t* q;
   const uint8_t* kv;
   const float* kv_scale;
   const int32_t* block_table;
   const int32_t* seqlens;
   const float* lse;
+  const float* q_scale;      // FP8: 2^e of every row
   float* weights;
-  void* ws;
-  float scale, decay;
-  int s_q, heads, causal, max_pages, num_pages;
+  char* ws;
+  uint32_t* counters;        // [units][2]
+  float* partial;            // [groups][units][256]
+  float sl2, decay;
+  int batch, s_q, heads, rows, causal, max_pages, num_pages, max_units;
 };
 
-template <bool kFp8>
-__global__ void __launch_bounds__(kWThreads) attn_weights_kernel(const WArgs a) {
-  extern __shared__ float sm[];
-  float* c_sm = sm;
-  float* q_sm = c_sm + MLA_PAGE_SIZE * kWRow;
-  float* part = q_sm + kWGroup * MLA_D_QK;
-  const int r = blockIdx.y, j = blockIdx.x, tid = threadIdx.x;
-  int t = a.seqlens[r];
-  const int cap = a.max_pages * MLA_PAGE_SIZE;
-  if ((t < 0 || t > cap) && j == 0 && tid == 0) flag_status(a.ws, kStatusBadSeqlen);
-  t = max(0, min(t, cap));
-  if (j * MLA_PAGE_SIZE >= t) return;
-  const int page = a.block_table[size_t(r) * a.max_pages + j];
-  const bool ok = page >= 0 && page < a.num_pages;
-  if (!ok && tid == 0) flag_status(a.ws, kStatusBadPage);
-  if (ok) {
-    for (int e = tid; e < MLA_PAGE_SIZE * MLA_D_QK; e += kWThreads) {
-      const int row = e / MLA_D_QK, col = e % MLA_D_QK;
-      float v;
-      if constexpr (kFp8) {
-        const uint8_t* pg = a.kv + size_t(page) * (MLA_PAGE_SIZE * (MLA_D_V + 2 * MLA_D_ROPE));
-        v = col < MLA_D_V ? e4m3_to_float(pg[row * MLA_D_V + col]) * a.kv_scale[size_t(page) * MLA_PAGE_SIZE + row]
-                          : bf16_bits_to_float(reinterpret_cast<const uint16_t*>(pg + MLA_PAGE_SIZE * MLA_D_V)[row * MLA_D_ROPE + col - MLA_D_V]);
-      } else {
-        v = bf16_bits_to_float(reinterpret_cast<const uint16_t*>(a.kv)[(size_t(page) * MLA_PAGE_SIZE + row) * MLA_D_QK + col]);
+// What every role derives from the lengths.
+struct Plan {
+  int r0, base0;             // first request with work for this pair, units before it
+  int64_t c0, c1;            // this pair's share, in unit x tile steps
+  int tile, tiles, groups;
+};
+
+struct Seg {
+  int r, t, row0, nh, u0, u1, unit0, group;
+  bool first_tile, first, last;   // of the request; of its group
+};
+
+__device__ __forceinline__ int w_len(const WArgs& a, int r) {
+  return max(0, min(a.seqlens[r], a.max_pages * MLA_PAGE_SIZE));
+}
+
+// Calls f for every (request, tile of rows, run of units) of this pair, in
+// order, until f returns false.
+template <class F>
+__device__ __forceinline__ bool each_seg(const WArgs& a, const Plan& p, F&& f) {
+  int64_t base = p.base0;
+  for (int r = p.r0; r < a.batch; ++r) {
+    if (base * p.tiles >= p.c1) break;
+    const int t = w_len(a, r), U = (t + kUnit - 1) / kUnit;
+    for (int s = 0; s < p.groups; ++s) {
+      const int ta = int(int64_t(s) * p.tiles / p.groups), tb = int(int64_t(s + 1) * p.tiles / p.groups), L = tb - ta;
+      const int64_t cb = base * p.tiles + int64_t(U) * ta;
+      const int u0 = p.c0 <= cb ? 0 : int(min(int64_t(U), (p.c0 - cb + L - 1) / L));
+      const int u1 = p.c1 <= cb ? 0 : int(min(int64_t(U), (p.c1 - cb + L - 1) / L));
+      if (u0 >= u1) continue;
+      for (int q = ta; q < tb; ++q) {
+        const int row0 = q * p.tile, left = min(p.tile, a.rows - row0);
+        if (!f(Seg{r, t, row0, ((left + 63) / 64) * 32, u0, u1, int(base), s, q == 0, q == ta, q == tb - 1})) return false;
       }
-      c_sm[row * kWRow + col] = v;
+    }
+    base += U;
+  }
+  return true;
+}
+
+struct WCtl {
+  volatile int32_t* abort;
+  uint32_t peer_abort;
+  char* ws;
+};
+
+__device__ __noinline__ void w_trip(const WCtl& c) {
+  *c.abort = 1;
+  st_cluster_u32(c.peer_abort, 1);
+  flag_status(c.ws, kStatusTimeout);
+}
+
+// Bounded wait; false when the pair is aborting.
+template <bool kSpin>
+__device__ __forceinline__ bool w_wait(const WCtl& c, uint32_t bar, uint32_t parity) {
+  auto once = [&] { return kSpin ? mbar_test_wait_cluster(bar, parity) : mbar_try_wait_cluster(bar, parity); };
+  if (once()) return true;
+  const uint64_t t0 = globaltimer();
+  for (uint32_t n = 1;; ++n) {
+    if (once()) return true;
+    if ((n & 15) == 0) {
+      if (*c.abort) return false;
+      if (globaltimer() - t0 > kWTimeoutNs) {
+        w_trip(c);
+        return false;
+      }
     }
   }
-  const int tok = tid % MLA_PAGE_SIZE, part_id = tid / MLA_PAGE_SIZE;   // 4 rows of a group per thread
-  const int pos = j * MLA_PAGE_SIZE + tok;
-  const int rows = a.s_q * a.heads;
-  float acc = 0.f;
-  for (int g = 0; ok && g < rows; g += kWGroup) {
-    __syncthreads();
-    for (int e = tid; e < kWGroup * MLA_D_QK; e += kWThreads) {
-      const int rho = g + e / MLA_D_QK;
-      q_sm[e] = rho < rows ? bf16_bits_to_float(a.q[(size_t(r) * rows + rho) * MLA_D_QK + e % MLA_D_QK]) : 0.f;
+}
+
+__device__ __forceinline__ uint64_t w_desc(uint32_t addr) {
+  return uint64_t((addr >> 4) & 0x3FFF) | (uint64_t(16 >> 4) << 16) | (uint64_t(1024 >> 4) << 32) | (1ull << 46) |
+         (2ull << 61);
+}
+
+// The pair's forms of the tensor core and copy instructions.  A load lands in
+// this CTA's shared memory and completes on the barrier `bar` (an address in
+// the cluster's window: the first CTA's).
+__device__ __forceinline__ void tma2_3d(uint32_t dst, const void* map, int c0, int c1, int c2, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], "
+      "[%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "r"(c2)
+      : "memory");
+}
+__device__ __forceinline__ void tma2_2d(uint32_t dst, const void* map, int c0, int c1, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];" ::
+          "r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1)
+      : "memory");
+}
+__device__ __forceinline__ void mma2_f16(uint32_t d, uint64_t ad, uint64_t bd, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(ad), "l"(bd), "r"(idesc), "r"(acc)
+      : "memory");
+}
+__device__ __forceinline__ void mma2_f8(uint32_t d, uint64_t ad, uint64_t bd, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(ad), "l"(bd), "r"(idesc), "r"(acc)
+      : "memory");
+}
+// Arrives on the barrier at this offset in both CTAs once the MMAs so far are done.
+__device__ __forceinline__ void commit2(uint32_t bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+      "h"(uint16_t(3))
+      : "memory");
+}
+
+// kind::f16 (bf16 A and B) and kind::f8f6f4 (e4m3), fp32 D, K-major, M = 256.
+__device__ __forceinline__ uint32_t idesc_bf16(int n) {
+  return (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t(n) >> 3) << 17) | ((256u >> 4) << 24);
+}
+__device__ __forceinline__ uint32_t idesc_e4m3(int n) {
+  return (1u << 4) | ((uint32_t(n) >> 3) << 17) | ((256u >> 4) << 24);
+}
+
+template <bool kFp8>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWThreads, 1)
+attn_weights_kernel(const __grid_constant__ CUtensorMap pool_map, const __grid_constant__ CUtensorMap rope_map,
+                    const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap q8_map, const WArgs a) {
+  constexpr int kStages = W<kFp8>::stages;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const uint32_t sbase = smem_u32(smem);
+  if ((sbase & 1023u) != 0) {   // the layout fills the SM: there is no room to align it
+    if (threadIdx.x == 0) flag_status(a.ws, kStatusWorkspace);
+    return;
+  }
+  WBars* bars = reinterpret_cast<WBars*>(smem);
+  auto bar = [&](const uint64_t& b) { return smem_u32(&b); };
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t rank = cluster_ctarank();
+  const int pairs = int(nclusters_x()), pair = int(cluster_id_x());
+
+  if (tid == 0) {
+    for (int s = 0; s < kWMaxStages; ++s) {
+      mbar_init(bar(bars->full[s]), 1);
+      mbar_init(bar(bars->empty[s]), 1);
     }
-    __syncthreads();
-    float s[4] = {0.f, 0.f, 0.f, 0.f};
-    for (int d = 0; d < MLA_D_QK; ++d) {
-      const float c = c_sm[tok * kWRow + d];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) s[k] = fmaf(q_sm[(part_id * 4 + k) * MLA_D_QK + d], c, s[k]);
+    for (int s = 0; s < 9; ++s) {
+      mbar_init(bar(bars->q_full[s]), 1);
+      mbar_init(bar(bars->q_free[s]), 1);
     }
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int rho = g + part_id * 4 + k;
-      if (rho >= rows || pos >= visible_len(t, a.s_q, rho / a.heads, a.causal)) continue;
-      const float l = a.lse[size_t(r) * rows + rho];
-      if (l != -INFINITY) acc += expf(s[k] * a.scale - l);
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(bar(bars->d_full[s]), 1);
+      mbar_init(bar(bars->d_empty[s]), 8);      // 4 warps of each CTA
+    }
+    mbar_init(bar(bars->done), 1);
+    bars->abort = 0;
+    fence_mbar_init();
+    tma_prefetch_desc(&pool_map);
+    tma_prefetch_desc(&q_map);
+    if (kFp8) {
+      tma_prefetch_desc(&rope_map);
+      tma_prefetch_desc(&q8_map);
     }
   }
-  part[part_id * MLA_PAGE_SIZE + tok] = acc;
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&bars->tmem_base))
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  }
+
+  // the units of all requests, and this pair's first request
+  Plan plan;
+  {
+    const int per = (a.batch + kWThreads - 1) / kWThreads;
+    const int ra = min(a.batch, tid * per), rb = min(a.batch, ra + per);
+    int mine = 0;
+    bool bad = false;
+    for (int r = ra; r < rb; ++r) {
+      const int t = a.seqlens[r];
+      bad |= t < 0 || t > a.max_pages * MLA_PAGE_SIZE;
+      mine += (w_len(a, r) + kUnit - 1) / kUnit;
+    }
+    if (bad && blockIdx.x == 0) flag_status(a.ws, kStatusBadSeqlen);
+    int inc = mine;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int u = __shfl_up_sync(0xffffffffu, inc, off);
+      if (lane >= off) inc += u;
+    }
+    if (lane == 31) bars->warp_sum[warp] = inc;
+    if (tid == 0) bars->r0 = a.batch;
+    __syncthreads();
+    int before = inc - mine, total = 0;
+#pragma unroll
+    for (int k = 0; k < kWThreads / 32; ++k) {
+      before += k < warp ? bars->warp_sum[k] : 0;
+      total += bars->warp_sum[k];
+    }
+    // tiles of rows: as many rows as a tile holds, but 128 where that leaves
+    // pairs without work
+    int tile = min(W<kFp8>::tile, (a.rows + 63) / 64 * 64);
+    if (tile > 128 && int64_t(total) * ((a.rows + tile - 1) / tile) < pairs) tile = 128;
+    plan.tile = tile;
+    plan.tiles = (a.rows + tile - 1) / tile;
+    plan.groups = total >= kSplitBelow * pairs || total == 0
+                      ? 1
+                      : min(min(plan.tiles, kMaxGroups), (kSplitBelow * pairs + total - 1) / total);
+    const int64_t cost = int64_t(total) * plan.tiles;
+    plan.c0 = cost * pair / pairs;
+    plan.c1 = cost * (pair + 1) / pairs;
+    if (plan.c0 < plan.c1 && before * int64_t(plan.tiles) <= plan.c0 && plan.c0 < (before + mine) * int64_t(plan.tiles)) {
+      int r = ra;
+      for (; r < rb; ++r) {
+        const int U = (w_len(a, r) + kUnit - 1) / kUnit;
+        if (plan.c0 < int64_t(before + U) * plan.tiles) break;
+        before += U;
+      }
+      bars->r0 = r;
+      bars->base0 = before;
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    plan.r0 = bars->r0;
+    plan.base0 = plan.r0 < a.batch ? bars->base0 : 0;
+  }
+  cluster_sync();
+  griddep_wait();   // FP8: the query's two parts
+
+  const uint32_t tmem = bars->tmem_base;
+  const uint32_t q_stride = uint32_t(plan.tile / 2) * 128u;     // one chunk of this CTA's half of the rows
+  const uint32_t q_base = sbase + kWHead, ring = q_base + 9u * q_stride;
+  const uint32_t nst = min(uint32_t(kWMaxStages), (kWSmem - kWHead - 9u * q_stride) / kWStage);
+  WCtl ctl{&bars->abort, mapa(smem_u32(&bars->abort), rank ^ 1u), a.ws};
+
+  if (warp == 0) {
+    // ---- producer (one lane)
+    if (lane == 0) {
+      const uint32_t full0 = mapa(bar(bars->full[0]), 0), q_full0 = mapa(bar(bars->q_full[0]), 0);
+      uint32_t slot = 0, ph = 0, segs = 0;
+      const bool ok = each_seg(a, plan, [&](const Seg& sg) {
+        const int pages = (sg.t + MLA_PAGE_SIZE - 1) / MLA_PAGE_SIZE;
+        const int32_t* bt = a.block_table + size_t(sg.r) * a.max_pages;
+        auto page_of = [&](int j) {   // -1: no such page; a bad id reads page 0, and its tokens receive nothing
+          if (j >= pages) return -1;
+          const int p = bt[j];
+          return p < 0 || p >= a.num_pages ? 0 : p;
+        };
+        const int row0 = sg.r * a.rows + sg.row0 + int(rank) * sg.nh;
+        int j = 4 * sg.u0 + 2 * int(rank);
+        int pa = page_of(j), pb = page_of(j + 1);
+        for (int u = sg.u0; u < sg.u1; ++u, j += 4) {
+          const int na = u + 1 < sg.u1 ? page_of(j + 4) : -1, nb = u + 1 < sg.u1 ? page_of(j + 5) : -1;
+          const uint32_t bytes = uint32_t(min(4, pages - 4 * u)) * kWBox;   // of both CTAs
+          for (int st = 0; st < kStages; ++st) {
+            if (u == sg.u0) {
+              if (!w_wait<true>(ctl, bar(bars->q_free[st]), (segs & 1u) ^ 1u)) return false;
+              const int chunks = kFp8 && st > 0 ? 2 : 1;
+              if (rank == 0) mbar_arrive_expect_tx(bar(bars->q_full[st]), uint32_t(chunks) * 2u * uint32_t(sg.nh) * 128u);
+              const uint32_t qb = q_full0 + 8u * uint32_t(st);
+              for (int y = 0; y < sg.nh; y += 32) {
+                const uint32_t dst = q_base + uint32_t(y) * 128u;
+                if (!kFp8) {
+                  tma2_2d(dst + uint32_t(st) * q_stride, &q_map, 64 * st, row0 + y, qb);
+                } else if (st == 0) {
+                  tma2_2d(dst, &q_map, MLA_D_V, row0 + y, qb);
+                } else {
+                  tma2_2d(dst + uint32_t(st) * q_stride, &q8_map, 128 * (st - 1), row0 + y, qb);
+                  tma2_2d(dst + uint32_t(st + 4) * q_stride, &q8_map, MLA_D_V + 128 * (st - 1), row0 + y, qb);
+                }
+              }
+            }
+            if (!w_wait<true>(ctl, bar(bars->empty[slot]), ph ^ 1u)) return false;
+            if (rank == 0) mbar_arrive_expect_tx(bar(bars->full[slot]), bytes);
+            const uint32_t dst = ring + slot * kWStage, fb = full0 + 8u * slot;
+            const CUtensorMap* map = kFp8 && st == 0 ? &rope_map : &pool_map;
+            const int col = kFp8 ? (st == 0 ? 0 : 128 * (st - 1)) : 64 * st;
+            if (pa >= 0) tma2_3d(dst, map, col, 0, pa, fb);
+            if (pb >= 0) tma2_3d(dst + kWBox, map, col, 0, pb, fb);
+            if (++slot == nst) {
+              slot = 0;
+              ph ^= 1u;
+            }
+          }
+          pa = na;
+          pb = nb;
+        }
+        ++segs;
+        return true;
+      });
+      if (!ok) {
+        // the pair is aborting: give this CTA's copies (which may complete on
+        // the other CTA's barrier) time to land before it leaves
+        const uint64_t t0 = globaltimer();
+        while (globaltimer() - t0 < 2000000ull) {
+        }
+      }
+    }
+  } else if (warp == 1 && rank == 0) {
+    // ---- MMA issuer (one lane of the pair's first CTA)
+    if (lane == 0) {
+      uint32_t slot = 0, ph = 0, segs = 0, units = 0;
+      const uint64_t ad0 = w_desc(ring), bd0 = w_desc(q_base);
+      const uint32_t qs = q_stride >> 4;
+      each_seg(a, plan, [&](const Seg& sg) {
+        const uint32_t ib = idesc_bf16(2 * sg.nh), i8 = idesc_e4m3(2 * sg.nh);
+        for (int u = sg.u0; u < sg.u1; ++u, ++units) {
+          const uint32_t buf = units & 1u, d = tmem + 256u * buf;
+          if (!w_wait<true>(ctl, bar(bars->d_empty[buf]), ((units >> 1) & 1u) ^ 1u)) return false;
+          tc_fence_after();
+#pragma unroll 1
+          for (int st = 0; st < kStages; ++st) {
+            if (u == sg.u0 && !w_wait<true>(ctl, bar(bars->q_full[st]), segs & 1u)) return false;
+            if (!w_wait<true>(ctl, bar(bars->full[slot]), ph)) return false;
+            tc_fence_after();
+            const uint64_t ad = ad0 + uint64_t(slot * (kWStage >> 4)), bd = bd0 + uint64_t(uint32_t(st) * qs);
+            if (!kFp8 || st == 0) {
+              const uint32_t dd = kFp8 ? d + 128u : d;
+#pragma unroll
+              for (int k = 0; k < 4; ++k) mma2_f16(dd, ad + 2u * k, bd + 2u * k, ib, st != 0 || k != 0 ? 1u : 0u);
+            } else {
+              const uint64_t bl = bd + uint64_t(4u * qs);
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                mma2_f8(d, ad + 2u * k, bd + 2u * k, i8, st != 1 || k != 0 ? 1u : 0u);
+                mma2_f8(d, ad + 2u * k, bl + 2u * k, i8, 1u);
+              }
+            }
+            commit2(bar(bars->empty[slot]));
+            if (u == sg.u1 - 1) commit2(bar(bars->q_free[st]));
+            if (++slot == nst) {
+              slot = 0;
+              ph ^= 1u;
+            }
+          }
+          commit2(bar(bars->d_full[buf]));
+        }
+        ++segs;
+        return true;
+      });
+      commit2(bar(bars->done));
+      const uint64_t t0 = globaltimer();
+      while (!mbar_try_wait_cluster(bar(bars->done), 0) && globaltimer() - t0 < kWTimeoutNs) {
+      }
+    }
+  } else if (warp >= 4) {
+    // ---- epilogue: thread i owns token i of this CTA's half of a unit
+    const int i = tid - 128;
+    const uint32_t lane_off = uint32_t((warp - 4) * 32) << 16;
+    const uint32_t d_empty0 = mapa(bar(bars->d_empty[0]), 0);
+    float* nlse = reinterpret_cast<float*>(smem + kOffNlse);      // per column: -lse in log2 units
+    float* cscale = nlse + 128;                                   // FP8: 2^e * scale
+    int* vis = reinterpret_cast<int*>(smem + kOffVis);            // per column: tokens it sees, 0 if it adds nothing
+    int* gmin = reinterpret_cast<int*>(smem + kOffGmin);          // of 32 columns
+    int* gmax = reinterpret_cast<int*>(smem + kOffGmax);
+    const int cap = a.max_pages * MLA_PAGE_SIZE;
+    uint32_t units = 0;
+    // A warp whose wait failed says so at the group's next barrier, where all
+    // four leave together.
+    bool ok = true, met = true;
+    each_seg(a, plan, [&](const Seg& sg) {
+      if (!named_bar_and(kEpiBar, 128, ok)) return met = false;   // everyone is done with the last tile's columns
+      for (int c = i; c < 2 * sg.nh; c += 128) {
+        const int row = sg.row0 + c;
+        int v = 0;
+        float nl = 0.f;
+        if (row < min(a.rows, sg.row0 + plan.tile)) {
+          const float l = a.lse[size_t(sg.r) * a.rows + row];
+          if (l != -INFINITY) {
+            v = min(sg.t, visible_len(sg.t, a.s_q, row / a.heads, a.causal));
+            nl = -l * 1.4426950408889634f;
+          }
+          if (kFp8) cscale[c] = a.q_scale[size_t(sg.r) * a.rows + row] * a.sl2;
+        } else if (kFp8) {
+          cscale[c] = 0.f;
+        }
+        nlse[c] = nl;
+        vis[c] = v;
+        const int lo = __reduce_min_sync(0xffffffffu, v), hi = __reduce_max_sync(0xffffffffu, v);
+        if (lane == 0) {
+          gmin[c >> 5] = lo;
+          gmax[c >> 5] = hi;
+        }
+      }
+      if (!named_bar_and(kEpiBar, 128, true)) return met = false;
+      const int ngroups = 2 * sg.nh / 32;
+      for (int u = sg.u0; u < sg.u1; ++u, ++units) {
+        const uint32_t buf = units & 1u, d = tmem + lane_off + 256u * buf;
+        const int pos0 = u * kUnit + int(rank) * kHalf, pos = pos0 + i;
+        const bool live = pos < sg.t;
+        bool good = false;
+        float old = 0.f, stok = 0.f;
+        float* acc_at = plan.groups == 1 ? a.weights + size_t(sg.r) * cap + pos
+                                         : a.partial + (size_t(sg.group) * a.max_units + sg.unit0 + u) * kUnit +
+                                               (pos - u * kUnit);
+        if (live) {
+          const int page = a.block_table[size_t(sg.r) * a.max_pages + pos / MLA_PAGE_SIZE];
+          good = page >= 0 && page < a.num_pages;
+          if (!good) flag_status(a.ws, kStatusBadPage);
+          if (kFp8 && good) stok = a.kv_scale[size_t(page) * MLA_PAGE_SIZE + pos % MLA_PAGE_SIZE];
+          if (plan.groups == 1 ? !sg.first_tile || a.decay != 0.f : !sg.first) old = *acc_at;
+          if (plan.groups == 1 && sg.first_tile) old *= a.decay;
+        }
+        const int top = min(sg.t, pos0 + kHalf) - 1;   // the half's last token
+        bool arrived = true;
+        if (lane == 0) arrived = w_wait<false>(ctl, bar(bars->d_full[buf]), (units >> 1) & 1u);
+        arrived = __shfl_sync(0xffffffffu, arrived ? 1 : 0, 0) != 0;
+        if (!arrived) {
+          ok = false;
+          break;
+        }
+        __syncwarp();
+        tc_fence_after();
+        float s0 = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
+        if (top >= pos0) {
+#pragma unroll 1
+          for (int g = 0; g < ngroups; ++g) {
+            const int seen = gmax[g];
+            if (pos0 >= seen) continue;   // no column of the group sees a token of this half
+            uint32_t x[32];
+            tmem_ld32(d + 32u * uint32_t(g), x);
+            float v[32];
+            if constexpr (kFp8) {
+              uint32_t y[32];
+              tmem_ld32(d + 128u + 32u * uint32_t(g), y);
+              tmem_wait_ld();
+#pragma unroll
+              for (int c = 0; c < 32; c += 4) {
+                const float4 nl = *reinterpret_cast<const float4*>(nlse + 32 * g + c);
+                const float4 cs = *reinterpret_cast<const float4*>(cscale + 32 * g + c);
+                v[c] = fmaf(__uint_as_float(x[c]), stok * cs.x, fmaf(__uint_as_float(y[c]), a.sl2, nl.x));
+                v[c + 1] = fmaf(__uint_as_float(x[c + 1]), stok * cs.y, fmaf(__uint_as_float(y[c + 1]), a.sl2, nl.y));
+                v[c + 2] = fmaf(__uint_as_float(x[c + 2]), stok * cs.z, fmaf(__uint_as_float(y[c + 2]), a.sl2, nl.z));
+                v[c + 3] = fmaf(__uint_as_float(x[c + 3]), stok * cs.w, fmaf(__uint_as_float(y[c + 3]), a.sl2, nl.w));
+              }
+            } else {
+              tmem_wait_ld();
+#pragma unroll
+              for (int c = 0; c < 32; c += 4) {
+                const float4 nl = *reinterpret_cast<const float4*>(nlse + 32 * g + c);
+                v[c] = fmaf(__uint_as_float(x[c]), a.sl2, nl.x);
+                v[c + 1] = fmaf(__uint_as_float(x[c + 1]), a.sl2, nl.y);
+                v[c + 2] = fmaf(__uint_as_float(x[c + 2]), a.sl2, nl.z);
+                v[c + 3] = fmaf(__uint_as_float(x[c + 3]), a.sl2, nl.w);
+              }
+            }
+            if (top < gmin[g]) {   // every column sees every token of this half
+#pragma unroll
+              for (int c = 0; c < 32; c += 4) {
+                s0 += ex2(v[c]);
+                s1 += ex2(v[c + 1]);
+                s2 += ex2(v[c + 2]);
+                s3 += ex2(v[c + 3]);
+              }
+            } else {
+#pragma unroll
+              for (int c = 0; c < 32; c += 4) {
+                const int4 n = *reinterpret_cast<const int4*>(vis + 32 * g + c);
+                s0 += pos < n.x ? ex2(v[c]) : 0.f;
+                s1 += pos < n.y ? ex2(v[c + 1]) : 0.f;
+                s2 += pos < n.z ? ex2(v[c + 2]) : 0.f;
+                s3 += pos < n.w ? ex2(v[c + 3]) : 0.f;
+              }
+            }
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_remote(d_empty0 + 8u * buf);
+        const float sum = good ? (s0 + s1) + (s2 + s3) : 0.f;
+        if (live) *acc_at = old + sum;
+        if (plan.groups > 1 && sg.last) {
+          // the group's sums of this unit are in: the last of the groups adds
+          // them up, in their order
+          __threadfence();
+          if (!named_bar_and(kEpiBar, 128, true)) return met = false;
+          uint32_t* cnt = a.counters + 2 * size_t(sg.unit0 + u) + rank;
+          if (i == 0) {
+            const bool last = atomicAdd(cnt, 1u) == uint32_t(plan.groups - 1);
+            if (last) *cnt = 0u;
+            bars->last = last;
+          }
+          if (!named_bar_and(kEpiBar, 128, true)) return met = false;
+          if (bars->last && live) {
+            __threadfence();
+            float* w = a.weights + size_t(sg.r) * cap + pos;
+            float s = a.decay != 0.f ? a.decay * *w : 0.f;
+            const float* part = a.partial + size_t(sg.unit0 + u) * kUnit + (pos - u * kUnit);
+            for (int k = 0; k < plan.groups; ++k) s += __ldcg(part + size_t(k) * a.max_units * kUnit);
+            *w = s;
+          }
+        }
+      }
+      return true;
+    });
+    if (met) named_bar_and(kEpiBar, 128, ok);
+  }
+
+  tc_fence_before();
   __syncthreads();
-  if (tid < MLA_PAGE_SIZE && pos < t) {
-    const float sum = (part[tid] + part[MLA_PAGE_SIZE + tid]) + (part[2 * MLA_PAGE_SIZE + tid] + part[3 * MLA_PAGE_SIZE + tid]);
-    float* w = a.weights + size_t(r) * cap + pos;
-    *w = a.decay != 0.f ? fmaf(a.decay, *w, sum) : sum;
+  cluster_sync();
+  if (warp == 1) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
   }
+  cluster_sync();
+}
+
+// FP8: the query rows' latent columns as two e4m3 parts, [row][hi 512, lo
+// 512], with a power-of-two scale per row.  One warp per row.
+__global__ void __launch_bounds__(256) split_query_kernel(const uint16_t* __restrict__ q, int rows, uint8_t* __restrict__ q8,
+                                                          float* __restrict__ q_scale) {
+  griddep_launch_dependents();
+  const int row = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  if (row >= rows) return;
+  const uint4* src = reinterpret_cast<const uint4*>(q + size_t(row) * MLA_D_QK) + 2 * lane;
+  const uint4 x = src[0], y = src[1];
+  float am = fmaxf(fmaxf(fmaxf(bf16_abs_max(x.x), bf16_abs_max(x.y)), fmaxf(bf16_abs_max(x.z), bf16_abs_max(x.w))),
+                   fmaxf(fmaxf(bf16_abs_max(y.x), bf16_abs_max(y.y)), fmaxf(bf16_abs_max(y.z), bf16_abs_max(y.w))));
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, off));
+  const int e = pow2_scale_exp(am);
+  const float inv = ldexpf(1.f, -e);
+  uint4 hi, lo;
+  split_e4m3x4(x.x, x.y, inv, &hi.x, &lo.x);
+  split_e4m3x4(x.z, x.w, inv, &hi.y, &lo.y);
+  split_e4m3x4(y.x, y.y, inv, &hi.z, &lo.z);
+  split_e4m3x4(y.z, y.w, inv, &hi.w, &lo.w);
+  uint4* dst = reinterpret_cast<uint4*>(q8 + size_t(row) * 1024);
+  dst[lane] = hi;
+  dst[32 + lane] = lo;
+  if (lane == 0) q_scale[row] = ldexpf(1.f, e);
+}
+
+// Workspace: [status][counters][groups' sums][FP8: query parts, scales].
+struct WLayout {
+  size_t counters, partial, q8, q_scale, total;
+  int max_units;
+};
+
+WLayout w_layout(const mla_shape_t* s, int num_sms) {
+  auto up = [](size_t x) { return (x + 255) & ~size_t(255); };
+  WLayout L;
+  const size_t rows = size_t(s->batch) * s->s_q * s->num_heads;
+  L.max_units = kSplitBelow * (num_sms >= 2 ? num_sms / 2 : 1);   // more units than this are never split
+  L.counters = kStatusBytes;
+  L.partial = up(L.counters + size_t(L.max_units) * 8);
+  L.q8 = up(L.partial + size_t(kMaxGroups) * L.max_units * kUnit * 4);
+  L.q_scale = L.total = L.q8;
+  if (s->cache_dtype == MLA_CACHE_FP8_E4M3) {
+    L.q_scale = up(L.q8 + rows * 1024);
+    L.total = up(L.q_scale + rows * 4);
+  }
+  return L;
 }
 
 }  // namespace
 
-size_t attn_weights_workspace_bytes(const mla_shape_t*, int) { return kStatusBytes; }
+size_t attn_weights_workspace_bytes(const mla_shape_t* shape, int num_sms) { return w_layout(shape, num_sms).total; }
 
 int launch_attn_weights(const mla_shape_t* shape, const void* q, const void* kv, const float* kv_scale,
                         const int32_t* block_table, const int32_t* seqlens, const float* lse, float scale, float decay,
-                        float* weights, void* ws, int, cudaStream_t stream) {
+                        float* weights, void* ws, int num_sms, cudaStream_t stream) {
   const bool fp8 = shape->cache_dtype == MLA_CACHE_FP8_E4M3;
+  const WLayout L = w_layout(shape, num_sms);
+  char* w = static_cast<char*>(ws);
+  const int rows = shape->s_q * shape->num_heads, q_rows = shape->batch * rows;
+  CUtensorMap pool_map, rope_map, q_map, q8_map;
+  if (!make_q_map(&q_map, q, q_rows, 32)) return MLA_ERR_CUDA;
+  if (fp8) {
+    if (!make_fp8_maps(&pool_map, &rope_map, kv, shape->num_pages)) return MLA_ERR_CUDA;
+    if (!make_byte_map(&q8_map, w + L.q8, q_rows, 1024, 32)) return MLA_ERR_CUDA;
+  } else {
+    if (!make_pool_map(&pool_map, kv, shape->num_pages)) return MLA_ERR_CUDA;
+    rope_map = pool_map;   // not read
+    q8_map = q_map;
+  }
   auto fn = fp8 ? &attn_weights_kernel<true> : &attn_weights_kernel<false>;
   if (!ensure_smem_attr(reinterpret_cast<const void*>(fn), int(kWSmem))) return MLA_ERR_CUDA;
-  WArgs a{static_cast<const uint16_t*>(q), static_cast<const uint8_t*>(kv), kv_scale, block_table, seqlens, lse, weights,
-          ws, scale, decay, shape->s_q, shape->num_heads, shape->causal, shape->max_pages_per_seq, shape->num_pages};
-  fn<<<dim3(unsigned(shape->max_pages_per_seq), unsigned(shape->batch)), kWThreads, kWSmem, stream>>>(a);
+  WArgs a{static_cast<const uint8_t*>(kv), kv_scale, block_table, seqlens, lse,
+          reinterpret_cast<const float*>(w + L.q_scale), weights, w, reinterpret_cast<uint32_t*>(w + L.counters),
+          reinterpret_cast<float*>(w + L.partial), scale * 1.4426950408889634f, decay, shape->batch, shape->s_q,
+          shape->num_heads, rows, shape->causal, shape->max_pages_per_seq, shape->num_pages, L.max_units};
+  if (fp8) {
+    split_query_kernel<<<(q_rows + 7) / 8, 256, 0, stream>>>(static_cast<const uint16_t*>(q), q_rows,
+                                                              reinterpret_cast<uint8_t*>(w + L.q8),
+                                                              reinterpret_cast<float*>(w + L.q_scale));
+    if (cudaGetLastError() != cudaSuccess) return MLA_ERR_CUDA;
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(unsigned(num_sms >= 2 ? num_sms / 2 * 2 : 2));
+  cfg.blockDim = dim3(kWThreads);
+  cfg.dynamicSmemBytes = kWSmem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = fp8 ? 1 : 0;
+  if (cudaLaunchKernelEx(&cfg, fn, pool_map, rope_map, q_map, q8_map, a) != cudaSuccess) return MLA_ERR_CUDA;
   return cudaGetLastError() == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
 }
 

@@ -19,6 +19,13 @@ struct TreeArgs {
   int mask_words = 0;
 };
 
+// Tensor maps of the cache pages and of row-major operands, all with the
+// 128-byte swizzle (decode_sm100.cu).  False when the driver refuses one.
+bool make_pool_map(CUtensorMap* map, const void* kv, int num_pages);
+bool make_fp8_maps(CUtensorMap* lat, CUtensorMap* rope, const void* kv, int num_pages);
+bool make_q_map(CUtensorMap* map, const void* q, int rows, int box_rows);
+bool make_byte_map(CUtensorMap* map, const void* base, int rows, int cols, int box_rows);
+
 // What prepare_decode_sm100 builds: the TMA descriptors over the page pool
 // and the query rows, and the launch geometry.  Plain data, valid for the
 // pointers and shape it was built from.

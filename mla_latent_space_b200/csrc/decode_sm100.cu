@@ -333,42 +333,6 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
       : "memory");
 }
 
-// Largest |value| of the two bf16 values of w.
-__device__ __forceinline__ float bf16_abs_max(uint32_t w) {
-  return fmaxf(fabsf(__uint_as_float(w << 16)), fabsf(__uint_as_float(w & 0xFFFF0000u)));
-}
-
-// e with am / 2^e <= 448 (e4m3's largest finite value), the smallest such
-// but at least -126, so that 2^-e stays finite (a row that small loses
-// nothing that matters: its values still land in e4m3's range); 0 for
-// am = 0 or a non-finite am (its NaN or infinity then reaches S as is).
-// frexpf gives the estimate; the loops correct it by at most a few steps
-// (at most 126 for a subnormal am) and always end.
-__device__ __forceinline__ int pow2_scale_exp(float am) {
-  if (!(am > 0.f) || !(am <= 3.402823466e38f)) return 0;
-  int e = 0;
-  frexpf(am * (1.f / 448.f), &e);   // am / 448 = m 2^e, 0.5 <= m < 1
-  while (ldexpf(am, -e) > 448.f) ++e;
-  while (e > -126 && ldexpf(am, -(e - 1)) <= 448.f) --e;
-  return e < -126 ? -126 : e;
-}
-
-// Four bf16 values (w01, w23, low half first) times `inv` (a power of two)
-// as e4m3 hi = RNE(x) and lo = RNE(x - hi), four bytes each, value 4k+j in
-// byte j.  x - hi is exact in fp32.
-__device__ __forceinline__ void split_e4m3x4(uint32_t w01, uint32_t w23, float inv, uint32_t* hi, uint32_t* lo) {
-  const float2 a = make_float2(__uint_as_float(w01 << 16) * inv, __uint_as_float(w01 & 0xFFFF0000u) * inv);
-  const float2 b = make_float2(__uint_as_float(w23 << 16) * inv, __uint_as_float(w23 & 0xFFFF0000u) * inv);
-  const __nv_fp8x2_storage_t ha = __nv_cvt_float2_to_fp8x2(a, __NV_SATFINITE, __NV_E4M3);
-  const __nv_fp8x2_storage_t hb = __nv_cvt_float2_to_fp8x2(b, __NV_SATFINITE, __NV_E4M3);
-  const float2 fa = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(ha, __NV_E4M3)));
-  const float2 fb = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(hb, __NV_E4M3)));
-  const __nv_fp8x2_storage_t la = __nv_cvt_float2_to_fp8x2(make_float2(a.x - fa.x, a.y - fa.y), __NV_SATFINITE, __NV_E4M3);
-  const __nv_fp8x2_storage_t lb = __nv_cvt_float2_to_fp8x2(make_float2(b.x - fb.x, b.y - fb.y), __NV_SATFINITE, __NV_E4M3);
-  *hi = uint32_t(ha) | (uint32_t(hb) << 16);
-  *lo = uint32_t(la) | (uint32_t(lb) << 16);
-}
-
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<uint32_t*>(&h);
@@ -1350,6 +1314,8 @@ decode_sm100_kernel(const __grid_constant__ CUtensorMap pool_map, const __grid_c
   cluster_sync();
 }
 
+}  // namespace
+
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
   static std::once_flag once;
@@ -1405,19 +1371,36 @@ bool make_fp8_maps(CUtensorMap* lat, CUtensorMap* rope, const void* kv, int num_
 }
 
 // Tensor map over the query rows [batch * s_q * heads][576] bf16: boxes of
-// 64 columns x 64 rows, 128-byte swizzle.  Rows past the end read as zero.
-bool make_q_map(CUtensorMap* map, const void* q, int rows) {
+// 64 columns x box_rows rows, 128-byte swizzle.  Rows past the end read as zero.
+bool make_q_map(CUtensorMap* map, const void* q, int rows, int box_rows) {
   auto fn = encode_fn();
   if (!fn) return false;
   cuuint64_t dims[2] = {cuuint64_t(MLA_D_QK), cuuint64_t(rows)};
   cuuint64_t strides[1] = {cuuint64_t(MLA_D_QK) * 2};
-  cuuint32_t box[2] = {64, 64};
+  cuuint32_t box[2] = {64, cuuint32_t(box_rows)};
   cuuint32_t estr[2] = {1, 1};
   CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(q), dims, strides, box, estr,
                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS;
 }
+
+// Tensor map over byte rows [rows][cols]: boxes of 128 bytes x box_rows rows,
+// 128-byte swizzle.  Rows past the end read as zero.
+bool make_byte_map(CUtensorMap* map, const void* base, int rows, int cols, int box_rows) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  cuuint64_t dims[2] = {cuuint64_t(cols), cuuint64_t(rows)};
+  cuuint64_t strides[1] = {cuuint64_t(cols)};
+  cuuint32_t box[2] = {128, cuuint32_t(box_rows)};
+  cuuint32_t estr[2] = {1, 1};
+  CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, estr,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS;
+}
+
+namespace {
 
 using DecodeKernel = void (*)(const CUtensorMap, const CUtensorMap, const CUtensorMap, const Params);
 DecodeKernel decode_kernel(bool fp8, bool tree) {
@@ -1441,7 +1424,7 @@ int prepare_decode_sm100(const mla_shape_t* shape, const void* q, const void* kv
     if (!make_pool_map(&pr->pool_map, kv, shape->num_pages)) return MLA_ERR_CUDA;
     pr->rope_map = pr->pool_map;   // not read
   }
-  if (!make_q_map(&pr->q_map, q, q_rows)) return MLA_ERR_CUDA;
+  if (!make_q_map(&pr->q_map, q, q_rows, 64)) return MLA_ERR_CUDA;
   if (!ensure_smem_attr(reinterpret_cast<const void*>(decode_kernel(pr->fp8, tree)), int(kSmemBytes)))
     return MLA_ERR_CUDA;
   return MLA_OK;

@@ -113,4 +113,40 @@ __device__ __forceinline__ float bf16_bits_to_float(uint16_t b) {
   return __uint_as_float(uint32_t(b) << 16);
 }
 
+// Largest |value| of the two bf16 values of w.
+__device__ __forceinline__ float bf16_abs_max(uint32_t w) {
+  return fmaxf(fabsf(__uint_as_float(w << 16)), fabsf(__uint_as_float(w & 0xFFFF0000u)));
+}
+
+// e with am / 2^e <= 448 (e4m3's largest finite value), the smallest such
+// but at least -126, so that 2^-e stays finite (a row that small loses
+// nothing that matters: its values still land in e4m3's range); 0 for
+// am = 0 or a non-finite am (its NaN or infinity then reaches S as is).
+// frexpf gives the estimate; the loops correct it by at most a few steps
+// (at most 126 for a subnormal am) and always end.
+__device__ __forceinline__ int pow2_scale_exp(float am) {
+  if (!(am > 0.f) || !(am <= 3.402823466e38f)) return 0;
+  int e = 0;
+  frexpf(am * (1.f / 448.f), &e);   // am / 448 = m 2^e, 0.5 <= m < 1
+  while (ldexpf(am, -e) > 448.f) ++e;
+  while (e > -126 && ldexpf(am, -(e - 1)) <= 448.f) --e;
+  return e < -126 ? -126 : e;
+}
+
+// Four bf16 values (w01, w23, low half first) times `inv` (a power of two)
+// as e4m3 hi = RNE(x) and lo = RNE(x - hi), four bytes each, value 4k+j in
+// byte j.  x - hi is exact in fp32.
+__device__ __forceinline__ void split_e4m3x4(uint32_t w01, uint32_t w23, float inv, uint32_t* hi, uint32_t* lo) {
+  const float2 a = make_float2(__uint_as_float(w01 << 16) * inv, __uint_as_float(w01 & 0xFFFF0000u) * inv);
+  const float2 b = make_float2(__uint_as_float(w23 << 16) * inv, __uint_as_float(w23 & 0xFFFF0000u) * inv);
+  const __nv_fp8x2_storage_t ha = __nv_cvt_float2_to_fp8x2(a, __NV_SATFINITE, __NV_E4M3);
+  const __nv_fp8x2_storage_t hb = __nv_cvt_float2_to_fp8x2(b, __NV_SATFINITE, __NV_E4M3);
+  const float2 fa = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(ha, __NV_E4M3)));
+  const float2 fb = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(hb, __NV_E4M3)));
+  const __nv_fp8x2_storage_t la = __nv_cvt_float2_to_fp8x2(make_float2(a.x - fa.x, a.y - fa.y), __NV_SATFINITE, __NV_E4M3);
+  const __nv_fp8x2_storage_t lb = __nv_cvt_float2_to_fp8x2(make_float2(b.x - fb.x, b.y - fb.y), __NV_SATFINITE, __NV_E4M3);
+  *hi = uint32_t(ha) | (uint32_t(hb) << 16);
+  *lo = uint32_t(la) | (uint32_t(lb) << 16);
+}
+
 }  // namespace mla

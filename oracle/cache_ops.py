@@ -64,10 +64,9 @@ def attn_weights(wl, lse: np.ndarray, decay: float, old: np.ndarray) -> np.ndarr
         new = np.zeros(t)
         for i in range(s):
             k = max(0, visible_len(t, s, i, wl.causal))
-            q = bf16_to_f64(wl.q[r, i])
-            for hh in range(h):
-                if lse[r, i, hh] != -np.inf:
-                    new[:k] += np.exp(wl.softmax_scale * (C[:k] @ q[hh]) - float(lse[r, i, hh]))
+            adds = lse[r, i] != -np.inf
+            x = wl.softmax_scale * (C[:k] @ bf16_to_f64(wl.q[r, i])[adds].T)
+            new[:k] += np.exp(x - lse[r, i][adds].astype(np.float64)).sum(axis=1)
         w[r, :t] = (decay * w[r, :t] if decay != 0.0 else 0.0) + new
     return w
 

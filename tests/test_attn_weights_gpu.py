@@ -96,6 +96,19 @@ def test_weights_over_many_units_and_repeated_calls_agree_bit_for_bit():
 
 
 @pytest.mark.parametrize("cache", ["bf16", "fp8"])
+def test_weights_when_groups_of_tiles_meet_in_the_workspace(cache):
+    # few units and many rows: each unit's tiles are shared between pairs, in groups of unequal size
+    wl = mw.make(3, 5, 120, [9000, 14000, 700], causal=True, seed=92, cache_dtype=cache)
+    lse, old = lse_of(wl), old_weights(wl)
+    acc, dev = mla.AttnWeights(shape_of(wl)), to_device(wl)
+    a, st = run(wl, lse, 0.75, old, acc, dev)
+    assert st == 0
+    assert_close(wl, a, lse, 0.75, old)
+    b, st = run(wl, lse, 0.75, old, acc, dev)
+    assert st == 0 and np.array_equal(a, b)
+
+
+@pytest.mark.parametrize("cache", ["bf16", "fp8"])
 def test_rows_without_lse_add_nothing_and_nan_behind_the_length_stays_out(cache):
     wl = mw.make(2, 4, 40, [100, 70], seed=86, cache_dtype=cache)
     lse, old = lse_of(wl), old_weights(wl)
