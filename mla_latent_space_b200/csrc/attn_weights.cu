@@ -16,10 +16,11 @@
 // while the pair's tokens pass through a ring of 16 KB stages (one 128-byte
 // column box of 128 tokens each), as deep as the rows leave room for.
 //
-// Roles (both CTAs; 256 threads): warp 0 streams pages and rows by TMA,
+// Roles (both CTAs; 384 threads): warp 0 streams pages and rows by TMA,
 // signalling the pair's first CTA; warp 1 of the first CTA issues the MMAs
-// into one of two TMEM accumulators; warps 4-7 drain the other one: one
-// fused multiply-add, one exp2 and one add a score.
+// into one of two TMEM accumulators; two warpgroups drain them, taking units
+// in turn: one fused multiply-add, one exp2 and one add a score.  One
+// warpgroup alone could not hide its own TMEM, exp2 and memory latencies.
 //
 // Split.  The work is (request, 256-token unit, tile of rows).  Every pair
 // counts the units from the lengths and takes an equal share, in the order
@@ -50,7 +51,8 @@ namespace {
 
 using namespace ptx;
 
-constexpr int kWThreads = 256;
+constexpr int kWThreads = 384;
+constexpr int kEpiThreads = 256;                 // warps 4-11
 constexpr int kUnit = 256;                       // tokens of a unit: 128 on each CTA
 constexpr int kHalf = kUnit / 2;
 constexpr uint32_t kWBox = 8192;                 // 64 tokens x 128 bytes
@@ -76,7 +78,6 @@ struct WBars {
   uint32_t tmem_base;
   int32_t abort;
   int32_t r0, base0, total, warp_sum[kWThreads / 32];
-  int32_t last;          // the epilogue's verdict: this CTA finished the unit
 };
 constexpr uint32_t kOffNlse = 512, kOffVis = 1536, kOffGmin = 2560, kOffGmax = 2592;
 static_assert(sizeof(WBars) <= kOffNlse, "barriers");
@@ -90,7 +91,7 @@ struct WArgs {
   const float* q_scale;      // FP8: 2^e of every row
   float* weights;
   char* ws;
-  uint32_t* counters;        // [units][2]
+  uint32_t* counters;        // [units][8]: one for each warp's 32 tokens of a unit
   float* partial;            // [groups][units][256]
   float sl2, decay;
   int batch, s_q, heads, rows, causal, max_pages, num_pages, max_units;
@@ -148,10 +149,11 @@ __device__ __noinline__ void w_trip(const WCtl& c) {
   flag_status(c.ws, kStatusTimeout);
 }
 
-// Bounded wait; false when the pair is aborting.
-template <bool kSpin>
+// Bounded wait; false when the pair is aborting.  (kCluster, below: the
+// barrier's arrivals are threads of either CTA.  The others are completed by
+// copies and MMAs alone.)
 __device__ __forceinline__ bool w_wait(const WCtl& c, uint32_t bar, uint32_t parity) {
-  auto once = [&] { return kSpin ? mbar_test_wait_cluster(bar, parity) : mbar_try_wait_cluster(bar, parity); };
+  auto once = [&] { return mbar_try_wait(bar, parity); };
   if (once()) return true;
   const uint64_t t0 = globaltimer();
   for (uint32_t n = 1;; ++n) {
@@ -160,6 +162,28 @@ __device__ __forceinline__ bool w_wait(const WCtl& c, uint32_t bar, uint32_t par
       if (*c.abort) return false;
       if (globaltimer() - t0 > kWTimeoutNs) {
         w_trip(c);
+        return false;
+      }
+    }
+  }
+}
+
+// The same for a whole warp: every lane polls and the warp leaves together,
+// so that the loop around it stays converged (its operands then stay in
+// uniform registers, and a wait costs the issuing warp half of what it does
+// to a lone lane).
+template <bool kCluster = false>
+__device__ __forceinline__ bool w_warp_wait(const WCtl& c, uint32_t bar, uint32_t parity) {
+  auto once = [&] { return kCluster ? mbar_test_wait_cluster(bar, parity) : mbar_test_wait(bar, parity); };
+  if (__all_sync(0xffffffffu, once())) return true;
+  const bool lead = (threadIdx.x & 31) == 0;
+  const uint64_t t0 = lead ? globaltimer() : 0ull;
+  for (uint32_t n = 1;; ++n) {
+    if (__all_sync(0xffffffffu, once())) return true;
+    if ((n & 15) == 0) {
+      const int stop = __shfl_sync(0xffffffffu, lead ? (*c.abort ? 1 : (globaltimer() - t0 > kWTimeoutNs ? 2 : 0)) : 0, 0);
+      if (stop != 0) {
+        if (stop == 2 && lead) w_trip(c);
         return false;
       }
     }
@@ -210,6 +234,14 @@ __device__ __forceinline__ void commit2(uint32_t bar) {
       : "memory");
 }
 
+// Arrives on a barrier of the pair's first CTA.  What it orders are this
+// warp's TMEM reads (complete, and fenced by tcgen05.fence), so the arrival
+// needs no wider scope: a release at cluster scope would make the warp wait
+// for its global loads and stores in flight.
+__device__ __forceinline__ void arrive_first(uint32_t cluster_bar) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
+}
+
 // kind::f16 (bf16 A and B) and kind::f8f6f4 (e4m3), fp32 D, K-major, M = 256.
 __device__ __forceinline__ uint32_t idesc_bf16(int n) {
   return (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t(n) >> 3) << 17) | ((256u >> 4) << 24);
@@ -246,7 +278,7 @@ attn_weights_kernel(const __grid_constant__ CUtensorMap pool_map, const __grid_c
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(bar(bars->d_full[s]), 1);
-      mbar_init(bar(bars->d_empty[s]), 8);      // 4 warps of each CTA
+      mbar_init(bar(bars->d_empty[s]), 8);      // a warpgroup of each CTA
     }
     mbar_init(bar(bars->done), 1);
     bars->abort = 0;
@@ -330,8 +362,10 @@ attn_weights_kernel(const __grid_constant__ CUtensorMap pool_map, const __grid_c
   WCtl ctl{&bars->abort, mapa(smem_u32(&bars->abort), rank ^ 1u), a.ws};
 
   if (warp == 0) {
-    // ---- producer (one lane)
-    if (lane == 0) {
+    // ---- producer warp (one lane issues)
+    {
+      const bool leader = elect_one();
+      const bool arm = leader && rank == 0;
       const uint32_t full0 = mapa(bar(bars->full[0]), 0), q_full0 = mapa(bar(bars->q_full[0]), 0);
       uint32_t slot = 0, ph = 0, segs = 0;
       const bool ok = each_seg(a, plan, [&](const Seg& sg) {
@@ -348,31 +382,38 @@ attn_weights_kernel(const __grid_constant__ CUtensorMap pool_map, const __grid_c
         for (int u = sg.u0; u < sg.u1; ++u, j += 4) {
           const int na = u + 1 < sg.u1 ? page_of(j + 4) : -1, nb = u + 1 < sg.u1 ? page_of(j + 5) : -1;
           const uint32_t bytes = uint32_t(min(4, pages - 4 * u)) * kWBox;   // of both CTAs
+#pragma unroll 1
           for (int st = 0; st < kStages; ++st) {
             if (u == sg.u0) {
-              if (!w_wait<true>(ctl, bar(bars->q_free[st]), (segs & 1u) ^ 1u)) return false;
+              if (!w_warp_wait(ctl, bar(bars->q_free[st]), (segs & 1u) ^ 1u)) return false;
               const int chunks = kFp8 && st > 0 ? 2 : 1;
-              if (rank == 0) mbar_arrive_expect_tx(bar(bars->q_full[st]), uint32_t(chunks) * 2u * uint32_t(sg.nh) * 128u);
+              if (arm) mbar_arrive_expect_tx(bar(bars->q_full[st]), uint32_t(chunks) * 2u * uint32_t(sg.nh) * 128u);
               const uint32_t qb = q_full0 + 8u * uint32_t(st);
-              for (int y = 0; y < sg.nh; y += 32) {
-                const uint32_t dst = q_base + uint32_t(y) * 128u;
-                if (!kFp8) {
-                  tma2_2d(dst + uint32_t(st) * q_stride, &q_map, 64 * st, row0 + y, qb);
-                } else if (st == 0) {
-                  tma2_2d(dst, &q_map, MLA_D_V, row0 + y, qb);
-                } else {
-                  tma2_2d(dst + uint32_t(st) * q_stride, &q8_map, 128 * (st - 1), row0 + y, qb);
-                  tma2_2d(dst + uint32_t(st + 4) * q_stride, &q8_map, MLA_D_V + 128 * (st - 1), row0 + y, qb);
+              if (leader) {
+                for (int y = 0; y < sg.nh; y += 32) {
+                  const uint32_t dst = q_base + uint32_t(y) * 128u;
+                  if (!kFp8) {
+                    tma2_2d(dst + uint32_t(st) * q_stride, &q_map, 64 * st, row0 + y, qb);
+                  } else if (st == 0) {
+                    tma2_2d(dst, &q_map, MLA_D_V, row0 + y, qb);
+                  } else {
+                    tma2_2d(dst + uint32_t(st) * q_stride, &q8_map, 128 * (st - 1), row0 + y, qb);
+                    tma2_2d(dst + uint32_t(st + 4) * q_stride, &q8_map, MLA_D_V + 128 * (st - 1), row0 + y, qb);
+                  }
                 }
               }
+              __syncwarp();
             }
-            if (!w_wait<true>(ctl, bar(bars->empty[slot]), ph ^ 1u)) return false;
-            if (rank == 0) mbar_arrive_expect_tx(bar(bars->full[slot]), bytes);
+            if (!w_warp_wait(ctl, bar(bars->empty[slot]), ph ^ 1u)) return false;
+            if (arm) mbar_arrive_expect_tx(bar(bars->full[slot]), bytes);
             const uint32_t dst = ring + slot * kWStage, fb = full0 + 8u * slot;
             const CUtensorMap* map = kFp8 && st == 0 ? &rope_map : &pool_map;
             const int col = kFp8 ? (st == 0 ? 0 : 128 * (st - 1)) : 64 * st;
-            if (pa >= 0) tma2_3d(dst, map, col, 0, pa, fb);
-            if (pb >= 0) tma2_3d(dst + kWBox, map, col, 0, pb, fb);
+            if (leader) {
+              if (pa >= 0) tma2_3d(dst, map, col, 0, pa, fb);
+              if (pb >= 0) tma2_3d(dst + kWBox, map, col, 0, pb, fb);
+            }
+            __syncwarp();
             if (++slot == nst) {
               slot = 0;
               ph ^= 1u;
@@ -393,8 +434,9 @@ attn_weights_kernel(const __grid_constant__ CUtensorMap pool_map, const __grid_c
       }
     }
   } else if (warp == 1 && rank == 0) {
-    // ---- MMA issuer (one lane of the pair's first CTA)
-    if (lane == 0) {
+    // ---- MMA issuer warp of the pair's first CTA (one lane issues)
+    {
+      const bool leader = elect_one();
       uint32_t slot = 0, ph = 0, segs = 0, units = 0;
       const uint64_t ad0 = w_desc(ring), bd0 = w_desc(q_base);
       const uint32_t qs = q_stride >> 4;
@@ -402,47 +444,54 @@ attn_weights_kernel(const __grid_constant__ CUtensorMap pool_map, const __grid_c
         const uint32_t ib = idesc_bf16(2 * sg.nh), i8 = idesc_e4m3(2 * sg.nh);
         for (int u = sg.u0; u < sg.u1; ++u, ++units) {
           const uint32_t buf = units & 1u, d = tmem + 256u * buf;
-          if (!w_wait<true>(ctl, bar(bars->d_empty[buf]), ((units >> 1) & 1u) ^ 1u)) return false;
+          if (!w_warp_wait<true>(ctl, bar(bars->d_empty[buf]), ((units >> 1) & 1u) ^ 1u)) return false;
           tc_fence_after();
 #pragma unroll 1
           for (int st = 0; st < kStages; ++st) {
-            if (u == sg.u0 && !w_wait<true>(ctl, bar(bars->q_full[st]), segs & 1u)) return false;
-            if (!w_wait<true>(ctl, bar(bars->full[slot]), ph)) return false;
+            if (u == sg.u0 && !w_warp_wait(ctl, bar(bars->q_full[st]), segs & 1u)) return false;
+            if (!w_warp_wait(ctl, bar(bars->full[slot]), ph)) return false;
             tc_fence_after();
             const uint64_t ad = ad0 + uint64_t(slot * (kWStage >> 4)), bd = bd0 + uint64_t(uint32_t(st) * qs);
-            if (!kFp8 || st == 0) {
-              const uint32_t dd = kFp8 ? d + 128u : d;
+            if (leader) {
+              if (!kFp8 || st == 0) {
+                const uint32_t dd = kFp8 ? d + 128u : d;
+                mma2_f16(dd, ad, bd, ib, st != 0 ? 1u : 0u);
 #pragma unroll
-              for (int k = 0; k < 4; ++k) mma2_f16(dd, ad + 2u * k, bd + 2u * k, ib, st != 0 || k != 0 ? 1u : 0u);
-            } else {
-              const uint64_t bl = bd + uint64_t(4u * qs);
+                for (int k = 1; k < 4; ++k) mma2_f16(dd, ad + 2u * k, bd + 2u * k, ib, 1u);
+              } else {
+                const uint64_t bl = bd + uint64_t(4u * qs);
 #pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                mma2_f8(d, ad + 2u * k, bd + 2u * k, i8, st != 1 || k != 0 ? 1u : 0u);
-                mma2_f8(d, ad + 2u * k, bl + 2u * k, i8, 1u);
+                for (int k = 0; k < 4; ++k) {
+                  mma2_f8(d, ad + 2u * k, bd + 2u * k, i8, st != 1 || k != 0 ? 1u : 0u);
+                  mma2_f8(d, ad + 2u * k, bl + 2u * k, i8, 1u);
+                }
               }
+              commit2(bar(bars->empty[slot]));
+              if (u == sg.u1 - 1) commit2(bar(bars->q_free[st]));
+              if (st == kStages - 1) commit2(bar(bars->d_full[buf]));
             }
-            commit2(bar(bars->empty[slot]));
-            if (u == sg.u1 - 1) commit2(bar(bars->q_free[st]));
+            __syncwarp();
             if (++slot == nst) {
               slot = 0;
               ph ^= 1u;
             }
           }
-          commit2(bar(bars->d_full[buf]));
         }
         ++segs;
         return true;
       });
-      commit2(bar(bars->done));
+      if (leader) commit2(bar(bars->done));
+      __syncwarp();
       const uint64_t t0 = globaltimer();
       while (!mbar_try_wait_cluster(bar(bars->done), 0) && globaltimer() - t0 < kWTimeoutNs) {
       }
     }
   } else if (warp >= 4) {
-    // ---- epilogue: thread i owns token i of this CTA's half of a unit
-    const int i = tid - 128;
-    const uint32_t lane_off = uint32_t((warp - 4) * 32) << 16;
+    // ---- epilogue: two warpgroups take a segment's units in turn (the same
+    // one of them for every tile of a unit); thread i of a warpgroup owns
+    // token i of this CTA's half
+    const int i = (tid - 128) & 127, wg = warp >= 8 ? 1 : 0, wq = warp & 3;
+    const uint32_t lane_off = uint32_t(wq * 32) << 16;
     const uint32_t d_empty0 = mapa(bar(bars->d_empty[0]), 0);
     float* nlse = reinterpret_cast<float*>(smem + kOffNlse);      // per column: -lse in log2 units
     float* cscale = nlse + 128;                                   // FP8: 2^e * scale
@@ -450,27 +499,29 @@ attn_weights_kernel(const __grid_constant__ CUtensorMap pool_map, const __grid_c
     int* gmin = reinterpret_cast<int*>(smem + kOffGmin);          // of 32 columns
     int* gmax = reinterpret_cast<int*>(smem + kOffGmax);
     const int cap = a.max_pages * MLA_PAGE_SIZE;
-    uint32_t units = 0;
+    uint32_t units = 0;   // before this segment
     // A warp whose wait failed says so at the group's next barrier, where all
-    // four leave together.
+    // eight leave together.  The barrier at a segment's start also keeps the
+    // parity waits sound: every earlier unit has been drained, by whichever
+    // warpgroup, before one of this segment is waited for.
     bool ok = true, met = true;
     each_seg(a, plan, [&](const Seg& sg) {
-      if (!named_bar_and(kEpiBar, 128, ok)) return met = false;   // everyone is done with the last tile's columns
-      for (int c = i; c < 2 * sg.nh; c += 128) {
+      if (!named_bar_and(kEpiBar, kEpiThreads, ok)) return met = false;
+      const int c = tid - 128;
+      if (c < 2 * sg.nh) {
         const int row = sg.row0 + c;
         int v = 0;
-        float nl = 0.f;
+        float nl = 0.f, cs = 0.f;
         if (row < min(a.rows, sg.row0 + plan.tile)) {
           const float l = a.lse[size_t(sg.r) * a.rows + row];
           if (l != -INFINITY) {
             v = min(sg.t, visible_len(sg.t, a.s_q, row / a.heads, a.causal));
             nl = -l * 1.4426950408889634f;
           }
-          if (kFp8) cscale[c] = a.q_scale[size_t(sg.r) * a.rows + row] * a.sl2;
-        } else if (kFp8) {
-          cscale[c] = 0.f;
+          if (kFp8) cs = a.q_scale[size_t(sg.r) * a.rows + row] * a.sl2;
         }
         nlse[c] = nl;
+        if (kFp8) cscale[c] = cs;
         vis[c] = v;
         const int lo = __reduce_min_sync(0xffffffffu, v), hi = __reduce_max_sync(0xffffffffu, v);
         if (lane == 0) {
@@ -478,28 +529,36 @@ attn_weights_kernel(const __grid_constant__ CUtensorMap pool_map, const __grid_c
           gmax[c >> 5] = hi;
         }
       }
-      if (!named_bar_and(kEpiBar, 128, true)) return met = false;
       const int ngroups = 2 * sg.nh / 32;
-      for (int u = sg.u0; u < sg.u1; ++u, ++units) {
-        const uint32_t buf = units & 1u, d = tmem + lane_off + 256u * buf;
+      const int32_t* bt = a.block_table + size_t(sg.r) * a.max_pages;
+      const bool direct = plan.groups == 1;
+      const bool reads_old = direct ? !sg.first_tile || a.decay != 0.f : !sg.first;
+      auto pos_of = [&](int u) { return u * kUnit + int(rank) * kHalf + i; };
+      auto sum_at = [&](int u) {   // where this thread's sum of unit u lives
+        return direct ? a.weights + size_t(sg.r) * cap + pos_of(u)
+                      : a.partial + (size_t(sg.group) * a.max_units + sg.unit0 + u) * kUnit + (pos_of(u) - u * kUnit);
+      };
+      // page id (-2: no token here), token scale and old sum of a unit; the
+      // ids are read two of this warpgroup's units ahead, the rest one
+      auto page_at = [&](int u) { return u < sg.u1 && pos_of(u) < sg.t ? bt[pos_of(u) / MLA_PAGE_SIZE] : -2; };
+      auto scale_at = [&](int u, int page) {
+        return kFp8 && page >= 0 && page < a.num_pages ? a.kv_scale[size_t(page) * MLA_PAGE_SIZE + pos_of(u) % MLA_PAGE_SIZE]
+                                                       : 0.f;
+      };
+      auto old_at = [&](int u, int page) { return reads_old && page != -2 ? *sum_at(u) : 0.f; };
+      const int ua = sg.u0 + ((wg ^ sg.r) & 1);
+      int page = page_at(ua), page1 = page_at(ua + 2);
+      float stok = scale_at(ua, page), old = old_at(ua, page);
+      if (!named_bar_and(kEpiBar, kEpiThreads, true)) return met = false;   // the columns are in place
+      for (int u = ua; u < sg.u1; u += 2) {
+        const int page2 = page_at(u + 4);
+        const float stok1 = scale_at(u + 2, page1), old1 = old_at(u + 2, page1);
+        const uint32_t n = units + uint32_t(u - sg.u0), buf = n & 1u, d = tmem + lane_off + 256u * buf;
         const int pos0 = u * kUnit + int(rank) * kHalf, pos = pos0 + i;
-        const bool live = pos < sg.t;
-        bool good = false;
-        float old = 0.f, stok = 0.f;
-        float* acc_at = plan.groups == 1 ? a.weights + size_t(sg.r) * cap + pos
-                                         : a.partial + (size_t(sg.group) * a.max_units + sg.unit0 + u) * kUnit +
-                                               (pos - u * kUnit);
-        if (live) {
-          const int page = a.block_table[size_t(sg.r) * a.max_pages + pos / MLA_PAGE_SIZE];
-          good = page >= 0 && page < a.num_pages;
-          if (!good) flag_status(a.ws, kStatusBadPage);
-          if (kFp8 && good) stok = a.kv_scale[size_t(page) * MLA_PAGE_SIZE + pos % MLA_PAGE_SIZE];
-          if (plan.groups == 1 ? !sg.first_tile || a.decay != 0.f : !sg.first) old = *acc_at;
-          if (plan.groups == 1 && sg.first_tile) old *= a.decay;
-        }
+        const bool live = page != -2, good = page >= 0 && page < a.num_pages;
         const int top = min(sg.t, pos0 + kHalf) - 1;   // the half's last token
         bool arrived = true;
-        if (lane == 0) arrived = w_wait<false>(ctl, bar(bars->d_full[buf]), (units >> 1) & 1u);
+        if (lane == 0) arrived = w_wait(ctl, bar(bars->d_full[buf]), (n >> 1) & 1u);
         arrived = __shfl_sync(0xffffffffu, arrived ? 1 : 0, 0) != 0;
         if (!arrived) {
           ok = false;
@@ -511,8 +570,7 @@ attn_weights_kernel(const __grid_constant__ CUtensorMap pool_map, const __grid_c
         if (top >= pos0) {
 #pragma unroll 1
           for (int g = 0; g < ngroups; ++g) {
-            const int seen = gmax[g];
-            if (pos0 >= seen) continue;   // no column of the group sees a token of this half
+            if (pos0 >= gmax[g]) continue;   // no column of the group sees a token of this half
             uint32_t x[32];
             tmem_ld32(d + 32u * uint32_t(g), x);
             float v[32];
@@ -521,75 +579,83 @@ attn_weights_kernel(const __grid_constant__ CUtensorMap pool_map, const __grid_c
               tmem_ld32(d + 128u + 32u * uint32_t(g), y);
               tmem_wait_ld();
 #pragma unroll
-              for (int c = 0; c < 32; c += 4) {
-                const float4 nl = *reinterpret_cast<const float4*>(nlse + 32 * g + c);
-                const float4 cs = *reinterpret_cast<const float4*>(cscale + 32 * g + c);
-                v[c] = fmaf(__uint_as_float(x[c]), stok * cs.x, fmaf(__uint_as_float(y[c]), a.sl2, nl.x));
-                v[c + 1] = fmaf(__uint_as_float(x[c + 1]), stok * cs.y, fmaf(__uint_as_float(y[c + 1]), a.sl2, nl.y));
-                v[c + 2] = fmaf(__uint_as_float(x[c + 2]), stok * cs.z, fmaf(__uint_as_float(y[c + 2]), a.sl2, nl.z));
-                v[c + 3] = fmaf(__uint_as_float(x[c + 3]), stok * cs.w, fmaf(__uint_as_float(y[c + 3]), a.sl2, nl.w));
+              for (int k = 0; k < 32; k += 4) {
+                const float4 nl = *reinterpret_cast<const float4*>(nlse + 32 * g + k);
+                const float4 cs = *reinterpret_cast<const float4*>(cscale + 32 * g + k);
+                v[k] = fmaf(__uint_as_float(x[k]), stok * cs.x, fmaf(__uint_as_float(y[k]), a.sl2, nl.x));
+                v[k + 1] = fmaf(__uint_as_float(x[k + 1]), stok * cs.y, fmaf(__uint_as_float(y[k + 1]), a.sl2, nl.y));
+                v[k + 2] = fmaf(__uint_as_float(x[k + 2]), stok * cs.z, fmaf(__uint_as_float(y[k + 2]), a.sl2, nl.z));
+                v[k + 3] = fmaf(__uint_as_float(x[k + 3]), stok * cs.w, fmaf(__uint_as_float(y[k + 3]), a.sl2, nl.w));
               }
             } else {
               tmem_wait_ld();
 #pragma unroll
-              for (int c = 0; c < 32; c += 4) {
-                const float4 nl = *reinterpret_cast<const float4*>(nlse + 32 * g + c);
-                v[c] = fmaf(__uint_as_float(x[c]), a.sl2, nl.x);
-                v[c + 1] = fmaf(__uint_as_float(x[c + 1]), a.sl2, nl.y);
-                v[c + 2] = fmaf(__uint_as_float(x[c + 2]), a.sl2, nl.z);
-                v[c + 3] = fmaf(__uint_as_float(x[c + 3]), a.sl2, nl.w);
+              for (int k = 0; k < 32; k += 4) {
+                const float4 nl = *reinterpret_cast<const float4*>(nlse + 32 * g + k);
+                v[k] = fmaf(__uint_as_float(x[k]), a.sl2, nl.x);
+                v[k + 1] = fmaf(__uint_as_float(x[k + 1]), a.sl2, nl.y);
+                v[k + 2] = fmaf(__uint_as_float(x[k + 2]), a.sl2, nl.z);
+                v[k + 3] = fmaf(__uint_as_float(x[k + 3]), a.sl2, nl.w);
               }
             }
             if (top < gmin[g]) {   // every column sees every token of this half
 #pragma unroll
-              for (int c = 0; c < 32; c += 4) {
-                s0 += ex2(v[c]);
-                s1 += ex2(v[c + 1]);
-                s2 += ex2(v[c + 2]);
-                s3 += ex2(v[c + 3]);
+              for (int k = 0; k < 32; k += 4) {
+                s0 += ex2(v[k]);
+                s1 += ex2(v[k + 1]);
+                s2 += ex2(v[k + 2]);
+                s3 += ex2(v[k + 3]);
               }
             } else {
 #pragma unroll
-              for (int c = 0; c < 32; c += 4) {
-                const int4 n = *reinterpret_cast<const int4*>(vis + 32 * g + c);
-                s0 += pos < n.x ? ex2(v[c]) : 0.f;
-                s1 += pos < n.y ? ex2(v[c + 1]) : 0.f;
-                s2 += pos < n.z ? ex2(v[c + 2]) : 0.f;
-                s3 += pos < n.w ? ex2(v[c + 3]) : 0.f;
+              for (int k = 0; k < 32; k += 4) {
+                const int4 w = *reinterpret_cast<const int4*>(vis + 32 * g + k);
+                s0 += pos < w.x ? ex2(v[k]) : 0.f;
+                s1 += pos < w.y ? ex2(v[k + 1]) : 0.f;
+                s2 += pos < w.z ? ex2(v[k + 2]) : 0.f;
+                s3 += pos < w.w ? ex2(v[k + 3]) : 0.f;
               }
             }
           }
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive_remote(d_empty0 + 8u * buf);
+        if (lane == 0) arrive_first(d_empty0 + 8u * buf);
         const float sum = good ? (s0 + s1) + (s2 + s3) : 0.f;
-        if (live) *acc_at = old + sum;
-        if (plan.groups > 1 && sg.last) {
-          // the group's sums of this unit are in: the last of the groups adds
-          // them up, in their order
+        if (live) {
+          if (!good) flag_status(a.ws, kStatusBadPage);
+          *sum_at(u) = fmaf(direct && sg.first_tile ? a.decay : 1.f, old, sum);
+        }
+        if (!direct && sg.last) {
+          // the group's sums of this unit are in: whichever warp is the last
+          // of the groups to say so adds its 32 tokens' sums up, in the
+          // groups' order
           __threadfence();
-          if (!named_bar_and(kEpiBar, 128, true)) return met = false;
-          uint32_t* cnt = a.counters + 2 * size_t(sg.unit0 + u) + rank;
-          if (i == 0) {
-            const bool last = atomicAdd(cnt, 1u) == uint32_t(plan.groups - 1);
-            if (last) *cnt = 0u;
-            bars->last = last;
-          }
-          if (!named_bar_and(kEpiBar, 128, true)) return met = false;
-          if (bars->last && live) {
+          __syncwarp();
+          uint32_t done = 0;
+          if (lane == 0) done = atomicAdd(a.counters + 8 * size_t(sg.unit0 + u) + 4 * rank + wq, 1u);
+          done = __shfl_sync(0xffffffffu, done, 0);
+          if (done == uint32_t(plan.groups - 1)) {
             __threadfence();
-            float* w = a.weights + size_t(sg.r) * cap + pos;
-            float s = a.decay != 0.f ? a.decay * *w : 0.f;
-            const float* part = a.partial + size_t(sg.unit0 + u) * kUnit + (pos - u * kUnit);
-            for (int k = 0; k < plan.groups; ++k) s += __ldcg(part + size_t(k) * a.max_units * kUnit);
-            *w = s;
+            if (lane == 0) a.counters[8 * size_t(sg.unit0 + u) + 4 * rank + wq] = 0u;
+            if (live) {
+              float* w = a.weights + size_t(sg.r) * cap + pos;
+              float s = a.decay != 0.f ? a.decay * *w : 0.f;
+              const float* part = a.partial + size_t(sg.unit0 + u) * kUnit + (pos - u * kUnit);
+              for (int k = 0; k < plan.groups; ++k) s += __ldcg(part + size_t(k) * a.max_units * kUnit);
+              *w = s;
+            }
           }
         }
+        page = page1;
+        page1 = page2;
+        stok = stok1;
+        old = old1;
       }
+      units += uint32_t(sg.u1 - sg.u0);
       return true;
     });
-    if (met) named_bar_and(kEpiBar, 128, ok);
+    if (met) named_bar_and(kEpiBar, kEpiThreads, ok);
   }
 
   tc_fence_before();
@@ -640,7 +706,7 @@ WLayout w_layout(const mla_shape_t* s, int num_sms) {
   const size_t rows = size_t(s->batch) * s->s_q * s->num_heads;
   L.max_units = kSplitBelow * (num_sms >= 2 ? num_sms / 2 : 1);   // more units than this are never split
   L.counters = kStatusBytes;
-  L.partial = up(L.counters + size_t(L.max_units) * 8);
+  L.partial = up(L.counters + size_t(L.max_units) * 32);
   L.q8 = up(L.partial + size_t(kMaxGroups) * L.max_units * kUnit * 4);
   L.q_scale = L.total = L.q8;
   if (s->cache_dtype == MLA_CACHE_FP8_E4M3) {
