@@ -149,29 +149,12 @@ __device__ __noinline__ void w_trip(const WCtl& c) {
   flag_status(c.ws, kStatusTimeout);
 }
 
-// Bounded wait; false when the pair is aborting.  (kCluster, below: the
-// barrier's arrivals are threads of either CTA.  The others are completed by
-// copies and MMAs alone.)
-__device__ __forceinline__ bool w_wait(const WCtl& c, uint32_t bar, uint32_t parity) {
-  auto once = [&] { return mbar_try_wait(bar, parity); };
-  if (once()) return true;
-  const uint64_t t0 = globaltimer();
-  for (uint32_t n = 1;; ++n) {
-    if (once()) return true;
-    if ((n & 15) == 0) {
-      if (*c.abort) return false;
-      if (globaltimer() - t0 > kWTimeoutNs) {
-        w_trip(c);
-        return false;
-      }
-    }
-  }
-}
-
-// The same for a whole warp: every lane polls and the warp leaves together,
-// so that the loop around it stays converged (its operands then stay in
-// uniform registers, and a wait costs the issuing warp half of what it does
-// to a lone lane).
+// Bounded wait of a warp; false when the pair is aborting.  Every lane polls,
+// without suspending, and the warp leaves together: the loop around it stays
+// converged (its operands then stay in uniform registers), and waking up from
+// a suspended wait cost the FP8 case 4 us in 77.  kCluster: the barrier's
+// arrivals are threads of either CTA; the others are completed by copies and
+// MMAs alone.
 template <bool kCluster = false>
 __device__ __forceinline__ bool w_warp_wait(const WCtl& c, uint32_t bar, uint32_t parity) {
   auto once = [&] { return kCluster ? mbar_test_wait_cluster(bar, parity) : mbar_test_wait(bar, parity); };
@@ -557,14 +540,10 @@ attn_weights_kernel(const __grid_constant__ CUtensorMap pool_map, const __grid_c
         const int pos0 = u * kUnit + int(rank) * kHalf, pos = pos0 + i;
         const bool live = page != -2, good = page >= 0 && page < a.num_pages;
         const int top = min(sg.t, pos0 + kHalf) - 1;   // the half's last token
-        bool arrived = true;
-        if (lane == 0) arrived = w_wait(ctl, bar(bars->d_full[buf]), (n >> 1) & 1u);
-        arrived = __shfl_sync(0xffffffffu, arrived ? 1 : 0, 0) != 0;
-        if (!arrived) {
+        if (!w_warp_wait(ctl, bar(bars->d_full[buf]), (n >> 1) & 1u)) {
           ok = false;
           break;
         }
-        __syncwarp();
         tc_fence_after();
         float s0 = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
         if (top >= pos0) {
