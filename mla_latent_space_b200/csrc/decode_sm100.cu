@@ -908,13 +908,23 @@ decode_sm100_kernel(const __grid_constant__ CUtensorMap pool_map, const __grid_c
           tc_fence_before();
           mbar_arrive(bar(bars->s_empty));
           float mh = -INFINITY;
+          if (kTree && __all_sync(0xffffffffu, (vis_lo & vis_hi) == 0xffffffffu)) {
+            // every row of the warp sees the whole page (the prefix, but for
+            // its last page): no test a column
 #pragma unroll
-          for (int c = 0; c < 32; ++c) {
-            const bool see0 = kTree ? ((vis_lo >> c) & 1u) != 0 : c < nv;
-            const bool see1 = kTree ? ((vis_hi >> c) & 1u) != 0 : c + 32 < nv;
-            x[c] = see0 ? x[c] * p.scale_log2 : -INFINITY;
-            x[c + 32] = see1 ? x[c + 32] * p.scale_log2 : -INFINITY;
-            mh = fmaxf(mh, fmaxf(x[c], x[c + 32]));
+            for (int c = 0; c < 64; ++c) {
+              x[c] *= p.scale_log2;
+              mh = fmaxf(mh, x[c]);
+            }
+          } else {
+#pragma unroll
+            for (int c = 0; c < 32; ++c) {
+              const bool see0 = kTree ? ((vis_lo >> c) & 1u) != 0 : c < nv;
+              const bool see1 = kTree ? ((vis_hi >> c) & 1u) != 0 : c + 32 < nv;
+              x[c] = see0 ? x[c] * p.scale_log2 : -INFINITY;
+              x[c + 32] = see1 ? x[c + 32] * p.scale_log2 : -INFINITY;
+              mh = fmaxf(mh, fmaxf(x[c], x[c + 32]));
+            }
           }
           asm volatile("st.shared.f32 [%0], %1;" ::"r"(xmax + 4u * uint32_t(g)), "f"(mh) : "memory");
           // staging is free once the previous block's copy has read it
