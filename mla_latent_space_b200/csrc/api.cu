@@ -48,7 +48,7 @@ cudaError_t launch_evict_select(const float* weights, int max_tokens, const int3
                                 cudaStream_t stream);
 size_t compact_workspace_bytes(const mla_shape_t* shape, int max_rows);
 int launch_compact(const mla_shape_t* shape, void* kv, float* kv_scale, const int32_t* block_table, const int32_t* src,
-                   const int32_t* src_lens, const int32_t* base, int max_rows, float* weights, void* ws,
+                   const int32_t* src_lens, const int32_t* base, int max_rows, float* weights, void* ws, int num_sms,
                    cudaStream_t stream);
 }  // namespace mla
 
@@ -617,7 +617,7 @@ int mla_cache_compact(const mla_shape_t* shape, void* kv_cache, float* kv_scale,
                       const int32_t* src, const int32_t* src_lens, const int32_t* base, int32_t max_rows, float* weights,
                       void* workspace, size_t workspace_bytes, void* stream) {
   CallRange range_("mla_cache_compact");
-  const int rc = check_shape(shape);
+  int rc = check_shape(shape);
   if (rc != MLA_OK) return rc;
   if (!kv_cache || !block_table || !src || !src_lens || !workspace || max_rows < 1) return MLA_ERR_INVALID_ARG;
   if (shape->cache_dtype == MLA_CACHE_FP8_E4M3 && !kv_scale) return MLA_ERR_INVALID_ARG;
@@ -627,7 +627,9 @@ int mla_cache_compact(const mla_shape_t* shape, void* kv_cache, float* kv_scale,
   const size_t need = mla_compact_workspace_bytes(shape, max_rows);
   if (need == 0) return MLA_ERR_UNSUPPORTED;
   if (workspace_bytes < need) return MLA_ERR_WORKSPACE;
-  return launch_compact(shape, kv_cache, kv_scale, block_table, src, src_lens, base, max_rows, weights, workspace,
+  int sms = 0;
+  if ((rc = device_sms(&sms)) != MLA_OK) return rc;
+  return launch_compact(shape, kv_cache, kv_scale, block_table, src, src_lens, base, max_rows, weights, workspace, sms,
                         static_cast<cudaStream_t>(stream));
 }
 

@@ -4,20 +4,24 @@
 // src ascends and never lies before its destination, so rows only move
 // towards the front.
 //
-// The list is cut into groups of rows.  A CTA takes the next group from a
-// counter, holds its rows in registers (four CTAs of 36 KB keep an SM's share
-// of the memory bandwidth in flight), says that it has read them, and writes
-// them once nobody still needs what lies there: the rows at its destinations
-// are the sources of earlier groups or of its own (src[k] >= base + k), and a
-// search of the list names them.  Groups are handed out in the order of the
-// list and a CTA waits only for reads of earlier ones, none of which wait for
-// anything, so every wait ends; the waits are bounded all the same.  Each row
-// is read once and written once: what bounds it is HBM.
+// The list is cut into groups of rows, dealt out in the list's order to the
+// CTAs of a cooperative launch (all of them run at once).  A CTA holds a
+// group's rows in registers, says that it has read them, and writes them once
+// the groups whose sources lie at its destinations have been read: those are
+// earlier groups or its own (src[k] >= base + k), two of them at most, and a
+// search of the list names them.  A CTA takes its groups in order and waits
+// only for earlier ones, so every wait ends; the waits are bounded all the
+// same.  Each row is read once and written once: what bounds it is HBM, as
+// long as enough rows are in flight: four CTAs an SM hold 36 KB each, and a
+// CTA resolves its next group's pages and search while the current rows are
+// on their way.  64 x 2048 of 4096 rows of BF16 (303 MB): 59 us; with a CTA a
+// group, handed out by a counter, 69.6; waiting for all earlier groups
+// instead of searching makes the CTAs queue behind each other: 94.
 //
-// Workspace: [status][counter][finished CTAs][epoch] in the first 256 bytes,
-// then one word a group, which holds the epoch of the last call that read the
-// group's rows (plus one).  The last CTA of a call resets the counters and
-// steps the epoch, so no call has to clear anything.
+// Workspace: [status][finished CTAs][epoch] in the first 256 bytes, then a
+// word a group: the epoch of the last call that read its rows.  Epochs only
+// grow, so no call has to clear anything: the last CTA to leave steps it.  A
+// list of one group needs none of this.
 #include <cuda_runtime.h>
 
 #include "kernel_util.cuh"
@@ -27,8 +31,9 @@ namespace mla {
 namespace {
 
 constexpr int kCompThreads = 256;
+constexpr int kCompCtas = 4;   // per SM
 constexpr uint64_t kCompTimeoutNs = 2000000000ull;
-enum CtlWord { C_STATUS = 0, C_TICKET, C_DONE, C_EPOCH };
+enum CtlWord { C_STATUS = 0, C_DONE, C_EPOCH };
 constexpr int kFp8LatBytes = MLA_PAGE_SIZE * MLA_D_V;
 constexpr int kFp8PageBytes = kFp8LatBytes + MLA_PAGE_SIZE * MLA_D_ROPE * 2;
 
@@ -71,14 +76,15 @@ __device__ __forceinline__ void st_release(uint32_t* p, uint32_t v) {
   asm volatile("st.release.gpu.global.u32 [%0], %1;" ::"l"(p), "r"(v) : "memory");
 }
 
-// Index of the first of the ascending src[0..n) that is >= x (n if none): a
-// search in steps of 256, by the whole CTA.
+// Index of the first of the ascending src[0..n) that is >= x (n if none), by
+// one warp in steps of 32 (256 threads a step would read 8 KB of list for
+// every 36 KB of rows).
 __device__ __forceinline__ int first_at_least(const int32_t* src, int n, int x) {
   int a = 0, b = n;
   while (a < b) {
-    const int step = (b - a + kCompThreads - 1) / kCompThreads;
-    const int64_t i = int64_t(a) + int64_t(threadIdx.x) * step;
-    const int c = __syncthreads_count(i < b && src[i] < x);
+    const int step = (b - a + 31) / 32;
+    const int64_t i = int64_t(a) + int64_t(threadIdx.x & 31) * step;
+    const int c = __popc(__ballot_sync(0xffffffffu, i < b && src[i] < x));
     if (c == 0) return a;
     b = int(min(int64_t(b), int64_t(a) + int64_t(c) * step));
     a = a + (c - 1) * step + 1;
@@ -87,111 +93,129 @@ __device__ __forceinline__ int first_at_least(const int32_t* src, int n, int x) 
 }
 
 template <bool kFp8>
-__global__ void __launch_bounds__(kCompThreads, 4) compact_kernel(const CompArgs a) {
+__global__ void __launch_bounds__(kCompThreads, kCompCtas) compact_kernel(const CompArgs a) {
   constexpr int kRows = kCompRows<kFp8>, kCh = kChunks<kFp8>, kPer = kRows * kCh / kCompThreads;
-  static_assert(kRows * kCh % kCompThreads == 0, "pieces");
-  __shared__ int64_t from[kRows], to[kRows];
-  __shared__ int pos_from[kRows], pos_to[kRows];
-  __shared__ uint32_t ticket_sh, epoch_sh;
+  static_assert(kRows * kCh % kCompThreads == 0 && kRows <= kCompThreads - 32, "pieces");
+  __shared__ int64_t from[2][kRows], to[2][kRows];
+  __shared__ int pos_from[2][kRows], pos_to[2][kRows];
+  __shared__ int first_sh[2];   // entries from here to the group's own may have their sources at its destinations
+  __shared__ uint32_t epoch_sh;
   const int tid = threadIdx.x;
-  if (tid == 0) {
-    epoch_sh = *const_cast<volatile uint32_t*>(a.ws + C_EPOCH) + 1u;
-    ticket_sh = atomicAdd(a.ws + C_TICKET, 1u);
-  }
-  __syncthreads();
-  const int r = int(ticket_sh % uint32_t(a.batch)), g = int(ticket_sh / uint32_t(a.batch));
-  const uint32_t epoch = epoch_sh;
-  uint32_t* flags = a.ws + kStatusBytes / 4 + size_t(r) * a.groups;
+  const bool solo = a.groups == 1;   // no other group's rows to wait for
+  const uint32_t total = uint32_t(a.batch) * uint32_t(a.groups);
   const int cap = a.max_pages * MLA_PAGE_SIZE;
-  int n = a.src_lens[r];
-  const int base = a.base != nullptr ? a.base[r] : 0;
-  bool bad = g == 0 && (n < 0 || n > a.max_rows || base < 0);
-  n = base < 0 ? 0 : max(0, min(n, a.max_rows));
-  const int32_t* src = a.src + size_t(r) * a.max_rows;
-  const int k0 = g * kRows;
-  if (k0 < n) {   // (uniform in the CTA)
-    bool moves = false;
-    if (tid < kRows) {
-      const int k = k0 + tid;
-      int64_t fr = -1;
-      if (k < n) {
-        const int p = src[k];
-        const int64_t d = int64_t(base) + k;
-        if (p < d || p >= cap || (k > 0 && p <= src[k - 1])) {
+  bool bad = false;
+
+  // Resolves the rows of group `item` into buffer b; true where this
+  // thread's row moves.  exists: whether the request's list reaches the group.
+  auto resolve = [&](uint32_t item, int b, bool* exists) -> bool {
+    const int r = int(item % uint32_t(a.batch)), g = int(item / uint32_t(a.batch));
+    int n = a.src_lens[r];
+    const int base = a.base != nullptr ? a.base[r] : 0;
+    if (g == 0 && (n < 0 || n > a.max_rows || base < 0)) bad = true;
+    n = base < 0 ? 0 : max(0, min(n, a.max_rows));
+    const int k0 = g * kRows;
+    const int32_t* src = a.src + size_t(r) * a.max_rows;
+    *exists = k0 < n;
+    if (tid >= kCompThreads - 32) {   // the last warp resolves no rows
+      const int first = g == 0 || k0 >= n || int64_t(base) + k0 >= cap ? k0 : first_at_least(src, k0, base + k0);
+      if (tid == kCompThreads - 32) first_sh[b] = first;
+    }
+    if (tid >= kRows) return false;
+    const int k = k0 + tid;
+    int64_t fr = -1;
+    if (k < n) {
+      const int p = src[k], before = k > 0 ? src[k - 1] : -1;
+      const int64_t d = int64_t(base) + k;
+      if (p < d || p >= cap || p <= before) {
+        bad = true;
+      } else if (p != d) {
+        const int32_t* bt = a.block_table + size_t(r) * a.max_pages;
+        const int pa = bt[p / MLA_PAGE_SIZE], pb = bt[d / MLA_PAGE_SIZE];
+        if (pa < 0 || pa >= a.num_pages || pb < 0 || pb >= a.num_pages) {
           bad = true;
-        } else if (p != d) {
-          const int pa = a.block_table[size_t(r) * a.max_pages + p / MLA_PAGE_SIZE];
-          const int pb = a.block_table[size_t(r) * a.max_pages + d / MLA_PAGE_SIZE];
-          if (pa < 0 || pa >= a.num_pages || pb < 0 || pb >= a.num_pages) {
-            bad = true;
-          } else {
-            fr = int64_t(pa) * MLA_PAGE_SIZE + p % MLA_PAGE_SIZE;
-            to[tid] = int64_t(pb) * MLA_PAGE_SIZE + d % MLA_PAGE_SIZE;
-            pos_from[tid] = p;
-            pos_to[tid] = int(d);
-            moves = true;
-          }
+        } else {
+          fr = int64_t(pa) * MLA_PAGE_SIZE + p % MLA_PAGE_SIZE;
+          to[b][tid] = int64_t(pb) * MLA_PAGE_SIZE + d % MLA_PAGE_SIZE;
+          pos_from[b][tid] = p;
+          pos_to[b][tid] = int(d);
         }
       }
-      from[tid] = fr;
     }
-    if (__syncthreads_or(moves)) {
-      uint4 v[kPer];
-      float sc = 0.f, w = 0.f;
+    from[b][tid] = fr;
+    return fr >= 0;
+  };
+
+  if (tid == 0) epoch_sh = solo ? 0u : *const_cast<volatile uint32_t*>(a.ws + C_EPOCH) + 1u;
+  uint32_t item = blockIdx.x;   // group item / batch of request item % batch
+  bool exists = false;
+  bool moves = __syncthreads_or(resolve(item, 0, &exists));   // (the grid has no CTA without an item)
+  const uint32_t epoch = epoch_sh;
+  for (int b = 0; item < total; b ^= 1) {   // (uniform in the CTA)
+    const int r = int(item % uint32_t(a.batch)), g = int(item / uint32_t(a.batch));
+    uint32_t* flags = a.ws + kStatusBytes / 4 + size_t(r) * a.groups;
+    uint4 v[kPer];
+    float sc = 0.f, w = 0.f;
+    const bool mine = moves && tid < kRows && from[b][tid] >= 0;
+    if (moves) {
 #pragma unroll
       for (int u = 0; u < kPer; ++u) {
         const int e = tid + kCompThreads * u, row = e / kCh;
-        if (from[row] >= 0) v[u] = __ldcg(reinterpret_cast<const uint4*>(a.kv + piece_offset<kFp8>(from[row], e % kCh)));
+        if (from[b][row] >= 0)
+          v[u] = __ldcg(reinterpret_cast<const uint4*>(a.kv + piece_offset<kFp8>(from[b][row], e % kCh)));
       }
-      const bool mine = tid < kRows && from[tid] >= 0;
       if (mine) {
-        if (kFp8) sc = __ldcg(a.kv_scale + from[tid]);
-        if (a.weights != nullptr) w = __ldcg(a.weights + size_t(r) * cap + pos_from[tid]);
+        if (kFp8) sc = __ldcg(a.kv_scale + from[b][tid]);
+        if (a.weights != nullptr) w = __ldcg(a.weights + size_t(r) * cap + pos_from[b][tid]);
       }
-      // while the rows are on their way: the earlier entries whose sources
-      // are this group's destinations are [first, first + kRows) at most
-      const int first = g == 0 || int64_t(base) + k0 >= cap ? k0 : first_at_least(src, k0, base + k0);
-      __threadfence();   // this thread's rows have been read ...
-      __syncthreads();
-      if (tid == 0) st_release(flags + g, epoch);   // ... and the CTA's
-      bool ok = true;
-      if (first < k0) {
-        const int g0 = first / kRows, g1 = (min(first + kRows, k0) - 1) / kRows;   // at most two groups, before g
-        if (tid <= g1 - g0) {
-          const uint32_t* f = flags + g0 + tid;
-          if (ld_acquire(f) != epoch) {
-            uint64_t t0, t1;
-            asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t0));
-            while (ld_acquire(f) != epoch) {
-              asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t1));
-              if (t1 - t0 > kCompTimeoutNs) {
-                ok = false;
-                atomicOr(reinterpret_cast<int32_t*>(a.ws), kStatusTimeout);
-                break;
-              }
+    }
+    // while they are on their way: the next group
+    const uint32_t next = item + gridDim.x;   // (below 2^32: both are below 2^31)
+    bool next_exists = false, next_moves = false;
+    if (next < total) next_moves = resolve(next, b ^ 1, &next_exists);
+    __threadfence();                                   // this thread's rows have been read ...
+    next_moves = __syncthreads_or(next_moves) != 0;    // ... and the CTA's
+    bool ok = true;
+    if (exists && !solo) {
+      if (tid == 0) st_release(flags + g, epoch);
+      const int first = first_sh[b];
+      if (moves && first < g * kRows) {
+        // the groups whose sources are this group's destinations: two at most
+        const int g0 = first / kRows, g1 = (min(first + kRows, g * kRows) - 1) / kRows;
+        if (tid <= g1 - g0 && ld_acquire(flags + g0 + tid) != epoch) {
+          uint64_t t0, t1;
+          asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t0));
+          while (ld_acquire(flags + g0 + tid) != epoch) {
+            asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t1));
+            if (t1 - t0 > kCompTimeoutNs) {
+              ok = false;
+              atomicOr(reinterpret_cast<int32_t*>(a.ws), kStatusTimeout);
+              break;
             }
           }
         }
         ok = __syncthreads_and(ok);
       }
-      if (ok) {
-#pragma unroll
-        for (int u = 0; u < kPer; ++u) {
-          const int e = tid + kCompThreads * u, row = e / kCh;
-          if (from[row] >= 0) *reinterpret_cast<uint4*>(a.kv + piece_offset<kFp8>(to[row], e % kCh)) = v[u];
-        }
-        if (mine) {
-          if (kFp8) a.kv_scale[to[tid]] = sc;
-          if (a.weights != nullptr) a.weights[size_t(r) * cap + pos_to[tid]] = w;
-        }
-      }
-    } else if (tid == 0) {
-      st_release(flags + g, epoch);   // rows that stay are nobody's destination
     }
+    if (moves && ok) {
+#pragma unroll
+      for (int u = 0; u < kPer; ++u) {
+        const int e = tid + kCompThreads * u, row = e / kCh;
+        if (from[b][row] >= 0)
+          *reinterpret_cast<uint4*>(a.kv + piece_offset<kFp8>(to[b][row], e % kCh)) = v[u];
+      }
+      if (mine) {
+        if (kFp8) a.kv_scale[to[b][tid]] = sc;
+        if (a.weights != nullptr) a.weights[size_t(r) * cap + pos_to[b][tid]] = w;
+      }
+    }
+    item = next;
+    exists = next_exists;
+    moves = next_moves;
+    __syncthreads();   // buffer b is filled again in the next turn
   }
   if (bad) atomicOr(reinterpret_cast<int32_t*>(a.ws), kStatusBadInput);
-  if (tid == 0 && atomicAdd(a.ws + C_DONE, 1u) == gridDim.x - 1) {
-    a.ws[C_TICKET] = 0u;
+  if (!solo && tid == 0 && atomicAdd(a.ws + C_DONE, 1u) == gridDim.x - 1) {
     a.ws[C_DONE] = 0u;
     a.ws[C_EPOCH] = epoch;
   }
@@ -204,22 +228,31 @@ int groups_for(bool fp8, int max_rows) {
 
 }  // namespace
 
-// 0: more groups than one launch takes.
+// 0: more groups than 31 bits count.
 size_t compact_workspace_bytes(const mla_shape_t* shape, int max_rows) {
-  const int64_t ctas = int64_t(shape->batch) * groups_for(shape->cache_dtype == MLA_CACHE_FP8_E4M3, max_rows);
-  return ctas < (int64_t(1) << 31) ? kStatusBytes + size_t(ctas) * 4 : 0;
+  const int64_t n = int64_t(shape->batch) * groups_for(shape->cache_dtype == MLA_CACHE_FP8_E4M3, max_rows);
+  return n < (int64_t(1) << 31) ? kStatusBytes + size_t(n) * 4 : 0;
 }
 
 int launch_compact(const mla_shape_t* shape, void* kv, float* kv_scale, const int32_t* block_table, const int32_t* src,
-                   const int32_t* src_lens, const int32_t* base, int max_rows, float* weights, void* ws,
+                   const int32_t* src_lens, const int32_t* base, int max_rows, float* weights, void* ws, int num_sms,
                    cudaStream_t stream) {
   const bool fp8 = shape->cache_dtype == MLA_CACHE_FP8_E4M3;
   const int groups = groups_for(fp8, max_rows);
   CompArgs a{static_cast<uint8_t*>(kv), kv_scale, block_table, src, src_lens, base, weights, static_cast<uint32_t*>(ws),
              shape->batch, groups, max_rows, shape->max_pages_per_seq, shape->num_pages};
-  const unsigned grid = unsigned(shape->batch) * unsigned(groups);
-  if (fp8) compact_kernel<true><<<grid, kCompThreads, 0, stream>>>(a);
-  else compact_kernel<false><<<grid, kCompThreads, 0, stream>>>(a);
+  // as many CTAs as are resident; where no CTA waits for another, one each
+  const int64_t total = int64_t(shape->batch) * groups, resident = kCompCtas * int64_t(num_sms);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(unsigned(groups == 1 || total < resident ? total : resident));
+  cfg.blockDim = dim3(kCompThreads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeCooperative;
+  attr[0].val.cooperative = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = groups == 1 ? 0 : 1;
+  if (cudaLaunchKernelEx(&cfg, fp8 ? &compact_kernel<true> : &compact_kernel<false>, a) != cudaSuccess) return MLA_ERR_CUDA;
   return cudaGetLastError() == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
 }
 
