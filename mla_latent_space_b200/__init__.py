@@ -128,12 +128,12 @@ def make_shape(batch, s_q, num_heads, max_pages_per_seq, num_pages, cache_dtype=
 
 
 def _ptr(t: Optional[torch.Tensor]):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _stream(stream=None):
-    s = torch.cuda.current_stream() if stream is None else stream
-    return ctypes.c_void_p(s.cuda_stream)
+    # the raw handle of the current stream, without building a Stream object (2 us a call)
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()) if stream is None else stream.cuda_stream
 
 
 def _check(rc: int, where: str):
@@ -150,8 +150,15 @@ def _need(t: torch.Tensor, name: str, dtype, shape=None):
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if shape is not None and t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+
+
+def _on_current_device(*tensors):
+    dev = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"every tensor must be on the current device (cuda:{dev}), got one on cuda:{t.get_device()}")
 
 
 def num_sms(device=None) -> int:
@@ -354,6 +361,7 @@ class TreeDecoder:
         _need(tree_mask, "tree_mask", torch.int64, (sh.batch, sh.s_q, (sh.s_q + 63) // 64))
         if draft_lens is not None:
             _need(draft_lens, "draft_lens", torch.int32, (sh.batch,))
+        _on_current_device(self.workspace, q, kv_cache, kv_scale, block_table, seqlens, tree_mask, out, lse, draft_lens)
         rc = lib().mla_tree_decode_fwd(ctypes.byref(sh), _ptr(q), _ptr(kv_cache), _ptr(kv_scale), _ptr(block_table),
                                        _ptr(seqlens), _ptr(draft_lens), _ptr(tree_mask), float(softmax_scale),
                                        _ptr(self.workspace), self.workspace.numel(), _ptr(out), _ptr(lse),
@@ -380,6 +388,7 @@ def mla_tree_mask(parents, tree_mask, draft_lens=None, device_status: Optional[t
         _need(draft_lens, "draft_lens", torch.int32, (b,))
     if device_status is not None:
         _need(device_status, "device_status", torch.int32)
+    _on_current_device(parents, tree_mask, draft_lens, device_status)
     _check(lib().mla_tree_mask(b, s, _ptr(parents), _ptr(draft_lens), _ptr(tree_mask), _ptr(device_status),
                                _stream(stream)), "mla_tree_mask")
 
@@ -406,6 +415,7 @@ class AttnWeights:
         sh = self.shape
         _check_decode_tensors(sh, q, kv_cache, kv_scale, block_table, seqlens, None, lse)
         _need(weights, "weights", torch.float32, (sh.batch, sh.max_pages_per_seq * PAGE))
+        _on_current_device(self.workspace, q, kv_cache, kv_scale, block_table, seqlens, lse, weights)
         rc = lib().mla_attn_weights_fwd(ctypes.byref(sh), _ptr(q), _ptr(kv_cache), _ptr(kv_scale), _ptr(block_table),
                                         _ptr(seqlens), _ptr(lse), float(softmax_scale), float(decay), _ptr(weights),
                                         _ptr(self.workspace), self.workspace.numel(), _stream(stream))
@@ -432,6 +442,7 @@ def mla_evict_select(weights, seqlens, budget, sink, recent, kept, kept_lens,
     _need(kept_lens, "kept_lens", torch.int32, (b,))
     if device_status is not None:
         _need(device_status, "device_status", torch.int32)
+    _on_current_device(weights, seqlens, kept, kept_lens, device_status)
     _check(lib().mla_evict_select(b, weights.shape[1], _ptr(weights), _ptr(seqlens), int(budget), int(sink), int(recent),
                                   _ptr(kept), _ptr(kept_lens), _ptr(device_status), _stream(stream)),
            "mla_evict_select")
@@ -466,6 +477,7 @@ class CacheCompactor:
             _need(base, "base", torch.int32, (sh.batch,))
         if weights is not None:
             _need(weights, "weights", torch.float32, (sh.batch, sh.max_pages_per_seq * PAGE))
+        _on_current_device(self.workspace, kv_cache, kv_scale, block_table, src, src_lens, base, weights)
         rc = lib().mla_cache_compact(ctypes.byref(sh), _ptr(kv_cache), _ptr(kv_scale), _ptr(block_table), _ptr(src),
                                      _ptr(src_lens), _ptr(base), self.max_rows, _ptr(weights), _ptr(self.workspace),
                                      self.workspace.numel(), _stream(stream))

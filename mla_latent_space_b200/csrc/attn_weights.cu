@@ -73,6 +73,18 @@ struct W {
   static constexpr int tile = kFp8 ? 128 : 256;  // most rows of a tile (FP8: two accumulators a buffer)
 };
 
+// BF16: the tensor core's fp32 accumulator drops what does not fit, always
+// towards zero.  Given a score x, the expected partial sum after k of the 36
+// steps is x k / 36 (columns in any order), a step loses a quarter of its
+// last place on average (the accumulator behaves as if it kept one bit more
+// than it returns), a last place is on average 0.72 * 2^-23 of the value, so
+// x comes out smaller by 18 * 0.25 * 0.72 * 2^-23 = 3.9e-7 of itself.  The
+// scale makes up for that: the weights' mean error goes from -1.4e-6 to
+// -1.7e-7 of themselves, their relative error from 1.9e-6 to 4.6e-7 (b=4,
+// h=128, up to 4096 tokens).  FP8's two shorter sums lose too little to
+// matter (-3e-7).
+constexpr double kTruncation = 4e-7;
+
 struct WBars {
   uint64_t full[kWMaxStages], empty[kWMaxStages], q_full[9], q_free[9], d_full[2], d_empty[2], done;
   uint32_t tmem_base;
@@ -720,7 +732,8 @@ int launch_attn_weights(const mla_shape_t* shape, const void* q, const void* kv,
   if (!ensure_smem_attr(reinterpret_cast<const void*>(fn), int(kWSmem))) return MLA_ERR_CUDA;
   WArgs a{static_cast<const uint8_t*>(kv), kv_scale, block_table, seqlens, lse,
           reinterpret_cast<const float*>(w + L.q_scale), weights, w, reinterpret_cast<uint32_t*>(w + L.counters),
-          reinterpret_cast<float*>(w + L.partial), scale * 1.4426950408889634f, decay, shape->batch, shape->s_q,
+          reinterpret_cast<float*>(w + L.partial),
+          float(double(scale) * 1.4426950408889634 * (fp8 ? 1.0 : 1.0 + kTruncation)), decay, shape->batch, shape->s_q,
           shape->num_heads, rows, shape->causal, shape->max_pages_per_seq, shape->num_pages, L.max_units};
   if (fp8) {
     split_query_kernel<<<(q_rows + 7) / 8, 256, 0, stream>>>(static_cast<const uint16_t*>(q), q_rows,

@@ -17,8 +17,11 @@
 // contiguous chunks over a cluster of 8 CTAs, which add up each other's
 // histograms and counts over distributed shared memory.  Rows too long even
 // for that re-read the weights through L2 in every pass.  What bounds it is
-// latency: a launch, one trip to memory, and five block- or cluster-wide
-// barriers.
+// latency: of the 16 us of two rows of 131072 tokens, 3.5 are the trip to
+// memory, 5 the digits' passes with their cluster barriers, 5 the ordered
+// output.  (Adding up equal bins within a warp before the shared-memory adds,
+// for the many weights that are zero, costs more than it saves: 30.7 us
+// against 26.6 at that stage.)
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 
@@ -40,6 +43,7 @@ constexpr int kSmemKeys = 48 * 1024;         // keys per CTA that fit beside the
 
 struct alignas(16) SelShared {
   int hist[kPasses][kBins];
+  int coarse[kPasses][kSelWarps];            // sums of 64 bins
   int warp_a[kSelWarps], warp_b[kSelWarps];
   int digit, need, count;                    // a pass's verdict
   int cta_gt, cta_eq;                        // this CTA's chunk: keys above thr, keys equal to it
@@ -50,19 +54,6 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
   if (w != w) return 0u;
   const uint32_t b = __float_as_uint(w + 0.f);
   return (b & 0x80000000u) ? ~b : b | 0x80000000u;
-}
-
-// hist[bin] += 1 for every lane with `in`.  The first such lane's bin is
-// added once for all lanes that share it: many weights are equal (zeros), and
-// 32 adds to one address would queue.
-__device__ __forceinline__ void count_bin(int* hist, bool in, int bin, int lane) {
-  const unsigned live = __ballot_sync(0xffffffffu, in);
-  if (live == 0) return;
-  const int first = __ffs(int(live)) - 1;
-  const int lead = __shfl_sync(0xffffffffu, bin, first);
-  const unsigned same = __ballot_sync(0xffffffffu, in && bin == lead);
-  if (lane == first) atomicAdd(&hist[lead], __popc(same));
-  else if (in && bin != lead) atomicAdd(&hist[bin], 1);
 }
 
 // Sum of v over the CTA's warps before this one, exclusive; all threads call.
@@ -101,11 +92,11 @@ evict_select_kernel(const float* __restrict__ weights, int max_tokens, const int
   const int chunk = ((t + kCtas - 1) / kCtas + 31) & ~31;
   const int lo = min(t, rank * chunk), n = min(t - lo, chunk);
   const int n32 = (n + 31) & ~31;
-  auto make_key = [&](int i) -> uint32_t {
+  auto key_of = [&](int i, float x) -> uint32_t {
     const int j = lo + i;
-    return j < sink || j >= t - recent ? 0xffffffffu : weight_key(w[j]);
+    return j < sink || j >= t - recent ? 0xffffffffu : weight_key(x);
   };
-  auto key_at = [&](int i) -> uint32_t { return kInSmem ? keys[i] : make_key(i); };
+  auto key_at = [&](int i) -> uint32_t { return kInSmem ? keys[i] : key_of(i, w[lo + i]); };
 
   uint32_t prefix = 0;
   int need = budget, shift = 21;
@@ -118,57 +109,79 @@ evict_select_kernel(const float* __restrict__ weights, int max_tokens, const int
       // the only pass over memory: eight loads in flight a thread
       constexpr int kU = 8;
       for (int i0 = tid; i0 < n32; i0 += kU * kSelThreads) {
-        uint32_t k[kU];
+        float x[kU];
 #pragma unroll
         for (int u = 0; u < kU; ++u) {
           const int i = i0 + u * kSelThreads;
-          k[u] = i < n ? make_key(i) : 0u;
+          x[u] = i < n ? w[lo + i] : 0.f;
         }
 #pragma unroll
         for (int u = 0; u < kU; ++u) {
           const int i = i0 + u * kSelThreads;
-          if (i - lane >= n32) break;   // uniform in the warp
-          if (kInSmem && i < n) keys[i] = k[u];
-          count_bin(hist, i < n, int(k[u] >> 21), lane);
+          if (i < n) {
+            const uint32_t k = key_of(i, x[u]);
+            if (kInSmem) keys[i] = k;
+            atomicAdd(&hist[k >> 21], 1);
+          }
         }
       }
     } else {
-      for (int i = tid; i < n32; i += kSelThreads) {
-        const uint32_t k = i < n ? key_at(i) : 0u;
-        count_bin(hist, i < n && (k & fixed) == prefix, int((k >> shift) & ((1u << bits) - 1u)), lane);
+#pragma unroll 4
+      for (int i = tid; i < n; i += kSelThreads) {
+        const uint32_t k = key_at(i);
+        if ((k & fixed) == prefix) atomicAdd(&hist[(k >> shift) & ((1u << bits) - 1u)], 1);
       }
+    }
+    // sums of 64 bins, then one warp finds the 64 and, within them, the bin
+    // that holds the last kept key, counting from the largest: of a cluster's
+    // histograms it reads 32 + 64 words each, not 2048
+    __syncthreads();
+    {
+      const int2 v = *reinterpret_cast<const int2*>(hist + 64 * warp + 2 * lane);
+      const int sum = __reduce_add_sync(0xffffffffu, v.x + v.y);
+      if (lane == 0) sh.coarse[pass][warp] = sum;
     }
     if constexpr (kCtas > 1) cg::this_cluster().sync();
     else __syncthreads();
-    // thread tid owns bins 2046 - 2 tid and 2047 - 2 tid: its prefix over
-    // the threads before it counts the keys of all larger bins
-    int hi_bin = 0, lo_bin = 0;
-    if constexpr (kCtas > 1) {
+    if (warp == 0) {
+      // keys in the lanes above (larger bins), exclusive
+      auto above_of = [&](int v) {
+        int inc = v;
 #pragma unroll
-      for (int c = 0; c < kCtas; ++c) {
-        const int2 v = *reinterpret_cast<const int2*>(cg::this_cluster().map_shared_rank(hist, c) + kBins - 2 - 2 * tid);
-        lo_bin += v.x;
-        hi_bin += v.y;
+        for (int off = 1; off < 32; off <<= 1) {
+          const int u = __shfl_down_sync(0xffffffffu, inc, off);
+          if (lane + off < 32) inc += u;
+        }
+        return inc - v;
+      };
+      int c = 0;
+      if constexpr (kCtas > 1) {
+#pragma unroll
+        for (int q = 0; q < kCtas; ++q) c += cg::this_cluster().map_shared_rank(sh.coarse[pass], q)[lane];
+      } else {
+        c = sh.coarse[pass][lane];
       }
-    } else {
-      const int2 v = *reinterpret_cast<const int2*>(hist + kBins - 2 - 2 * tid);
-      lo_bin = v.x;
-      hi_bin = v.y;
-    }
-    int inc = lo_bin + hi_bin;
+      int above = above_of(c);
+      const int big = __ffs(int(__ballot_sync(0xffffffffu, above < need && need <= above + c))) - 1;
+      above = __shfl_sync(0xffffffffu, above, big);
+      int2 f = make_int2(0, 0);   // bins 64 big + 2 lane, + 1
+      if constexpr (kCtas > 1) {
 #pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-      const int u = __shfl_up_sync(0xffffffffu, inc, off);
-      if (lane >= off) inc += u;
-    }
-    if (lane == 31) sh.warp_a[warp] = inc;
-    __syncthreads();
-    const int above = warp_prefix(sh.warp_a, warp, lane) + inc - lo_bin - hi_bin;   // keys in larger bins
-    if (above < need && need <= above + hi_bin + lo_bin) {
-      const bool in_hi = need <= above + hi_bin;
-      sh.digit = in_hi ? kBins - 1 - 2 * tid : kBins - 2 - 2 * tid;
-      sh.need = in_hi ? need - above : need - above - hi_bin;
-      sh.count = in_hi ? hi_bin : lo_bin;
+        for (int q = 0; q < kCtas; ++q) {
+          const int2 v = *reinterpret_cast<const int2*>(cg::this_cluster().map_shared_rank(hist, q) + 64 * big + 2 * lane);
+          f.x += v.x;
+          f.y += v.y;
+        }
+      } else {
+        f = *reinterpret_cast<const int2*>(hist + 64 * big + 2 * lane);
+      }
+      above += above_of(f.x + f.y);
+      if (above < need && need <= above + f.x + f.y) {   // one lane
+        const bool in_hi = need <= above + f.y;
+        sh.digit = 64 * big + 2 * lane + (in_hi ? 1 : 0);
+        sh.need = in_hi ? need - above : need - above - f.y;
+        sh.count = in_hi ? f.y : f.x;
+      }
     }
     __syncthreads();
     prefix |= uint32_t(sh.digit) << shift;
@@ -186,11 +199,14 @@ evict_select_kernel(const float* __restrict__ weights, int max_tokens, const int
   const int run = (n32 / 32 + kSelWarps - 1) / kSelWarps * 32;
   const int b = min(n32, warp * run), e = min(n32, b + run);
   int gt = 0, eq = 0;
-  for (int i = b + lane; i < e; i += 32) {
-    const uint32_t k = i < n ? key_at(i) : 0u;
-    gt += __popc(__ballot_sync(0xffffffffu, i < n && k > thr));
-    eq += __popc(__ballot_sync(0xffffffffu, i < n && k == thr));
+#pragma unroll 4
+  for (int i = b + lane; i < min(e, n); i += 32) {
+    const uint32_t k = key_at(i);
+    gt += k > thr;
+    eq += k == thr;
   }
+  gt = __reduce_add_sync(0xffffffffu, gt);
+  eq = __reduce_add_sync(0xffffffffu, eq);
   if (lane == 0) {
     sh.warp_a[warp] = gt;
     sh.warp_b[warp] = eq;
@@ -213,6 +229,7 @@ evict_select_kernel(const float* __restrict__ weights, int max_tokens, const int
   }
   at += min(eq_rank, need);
   const unsigned below = (1u << lane) - 1u;
+#pragma unroll 4
   for (int i = b + lane; i < e; i += 32) {
     const uint32_t k = i < n ? key_at(i) : 0u;
     const bool is_eq = i < n && k == thr;

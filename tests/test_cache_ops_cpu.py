@@ -116,6 +116,19 @@ def test_binding_refuses_what_the_kernels_do_not_take():
         mla.mla_evict_select(torch.zeros((2, 8)), t[:, 0], 4, 0, 0, t, t[:, 0])
 
 
+def test_binding_refuses_tensors_of_another_device(monkeypatch):
+    class On:
+        def __init__(self, index):
+            self.index = index
+
+        def get_device(self):
+            return self.index
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    mla._on_current_device(On(0), None, On(0))
+    with pytest.raises(ValueError):
+        mla._on_current_device(On(0), On(1))
+
+
 # ---- the oracle's own pins ----------------------------------------------------
 
 def test_oracle_tree_mask_of_chain_star_and_bad_parents():
