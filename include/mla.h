@@ -326,7 +326,7 @@ int mla_tree_mask(int32_t batch, int32_t s_q, const int32_t* parents, const int3
  * decay = 0 does not read the old weights.  The sums are fp32, in an order
  * that does not change from call to call.
  *   shape, q, kv_cache, kv_scale, block_table, seqlens, softmax_scale: as for
- *             mla_decode_fwd; batch <= 65535.
+ *             mla_decode_fwd; batch <= 65535, s_q <= 65534.
  *   lse     : fp32 [batch, s_q, num_heads].
  *   weights : fp32 [batch, max_pages_per_seq * 64].
  *   workspace: mla_attn_weights_workspace_bytes(shape, num_sms of this device)

@@ -404,7 +404,7 @@ class AttnWeights:
         self.n_sms = num_sms(self.device)
         nb = int(lib().mla_attn_weights_workspace_bytes(ctypes.byref(shape), self.n_sms))
         if nb == 0:
-            raise MLAError(-2, "AttnWeights: shape not supported (batch <= 65535)")
+            raise MLAError(-2, "AttnWeights: shape not supported (batch <= 65535, s_q <= 65534)")
         self.workspace = torch.zeros(nb, dtype=torch.uint8, device=self.device)
 
     def accumulate(self, q, kv_cache, block_table, seqlens, lse, softmax_scale, decay, weights, kv_scale=None,

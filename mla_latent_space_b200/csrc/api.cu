@@ -563,7 +563,7 @@ int mla_tree_get_device_status(const mla_shape_t* shape, int num_sms, void* work
 }
 
 size_t mla_attn_weights_workspace_bytes(const mla_shape_t* shape, int num_sms) {
-  if (check_shape(shape) != MLA_OK || shape->batch > 65535 || num_sms < 1) return 0;
+  if (check_shape(shape) != MLA_OK || shape->batch > 65535 || shape->s_q > 65534 || num_sms < 1) return 0;
   return attn_weights_workspace_bytes(shape, num_sms);
 }
 
@@ -579,7 +579,7 @@ int mla_attn_weights_fwd(const mla_shape_t* shape, const void* q, const void* kv
       !aligned(seqlens, 4) || !aligned(lse, 4) || !aligned(weights, 4) || !aligned(workspace, 256))
     return MLA_ERR_INVALID_ARG;
   if (!std::isfinite(softmax_scale) || !std::isfinite(decay)) return MLA_ERR_INVALID_ARG;
-  if (shape->batch > 65535) return MLA_ERR_UNSUPPORTED;
+  if (shape->batch > 65535 || shape->s_q > 65534) return MLA_ERR_UNSUPPORTED;
   int sms = 0;
   if ((rc = device_sms(&sms)) != MLA_OK) return rc;
   if (workspace_bytes < mla_attn_weights_workspace_bytes(shape, sms)) return MLA_ERR_WORKSPACE;

@@ -18,9 +18,10 @@
 //
 // Roles (both CTAs; 384 threads): warp 0 streams pages and rows by TMA,
 // signalling the pair's first CTA; warp 1 of the first CTA issues the MMAs
-// into one of two TMEM accumulators; two warpgroups drain them, taking units
-// in turn: one fused multiply-add, one exp2 and one add a score.  One
-// warpgroup alone could not hide its own TMEM, exp2 and memory latencies.
+// into one of two TMEM accumulators; two warpgroups drain them, each half of
+// the columns: one fused multiply-add, one exp2 and one add a score.  (One
+// warpgroup alone could not hide its own TMEM, exp2 and memory latencies;
+// two that take units in turn hold each accumulator twice as long.)
 //
 // Split.  The work is (request, 256-token unit, tile of rows).  Every pair
 // counts the units from the lengths and takes an equal share, in the order
@@ -86,13 +87,18 @@ struct W {
 constexpr double kTruncation = 4e-7;
 
 struct WBars {
-  uint64_t full[kWMaxStages], empty[kWMaxStages], q_full[9], q_free[9], d_full[2], d_empty[2], done;
+  uint64_t full[kWMaxStages], empty[kWMaxStages], q_full[9], q_free[9], d_full[2], d_empty[2], part_full[2], done;
   uint32_t tmem_base;
   int32_t abort;
-  int32_t r0, base0, total, warp_sum[kWThreads / 32];
+  int32_t r0, base0;
 };
-constexpr uint32_t kOffNlse = 512, kOffVis = 1536, kOffGmin = 2560, kOffGmax = 2592;
-static_assert(sizeof(WBars) <= kOffNlse, "barriers");
+// Behind the barriers: the units of each warp's requests (at the start), then
+// per 32 columns the fewest and the most tokens one of them sees; per column
+// -lse (FP8: and the row's scale) and what it sees; the second warpgroup's
+// sums, [accumulator][token].
+constexpr uint32_t kOffWarpSum = 448, kOffGmin = 448, kOffGmax = 480, kOffNlse = 512, kOffHid = 1536, kOffPart = 2048;
+static_assert(sizeof(WBars) <= kOffGmin && kOffPart + 1024 <= kWHead, "head");
+constexpr uint16_t kDead = 0xffff;   // a column that adds nothing
 
 struct WArgs {
   const uint8_t* kv;
@@ -273,7 +279,8 @@ attn_weights_kernel(const __grid_constant__ CUtensorMap pool_map, const __grid_c
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(bar(bars->d_full[s]), 1);
-      mbar_init(bar(bars->d_empty[s]), 8);      // a warpgroup of each CTA
+      mbar_init(bar(bars->d_empty[s]), 16);     // 8 warps of each CTA
+      mbar_init(bar(bars->part_full[s]), 4);    // the second warpgroup's warps
     }
     mbar_init(bar(bars->done), 1);
     bars->abort = 0;
@@ -310,14 +317,15 @@ attn_weights_kernel(const __grid_constant__ CUtensorMap pool_map, const __grid_c
       const int u = __shfl_up_sync(0xffffffffu, inc, off);
       if (lane >= off) inc += u;
     }
-    if (lane == 31) bars->warp_sum[warp] = inc;
+    int* warp_sum = reinterpret_cast<int*>(smem + kOffWarpSum);
+    if (lane == 31) warp_sum[warp] = inc;
     if (tid == 0) bars->r0 = a.batch;
     __syncthreads();
     int before = inc - mine, total = 0;
 #pragma unroll
     for (int k = 0; k < kWThreads / 32; ++k) {
-      before += k < warp ? bars->warp_sum[k] : 0;
-      total += bars->warp_sum[k];
+      before += k < warp ? warp_sum[k] : 0;
+      total += warp_sum[k];
     }
     // tiles of rows: as many rows as a tile holds, but 128 where that leaves
     // pairs without work
@@ -482,42 +490,43 @@ attn_weights_kernel(const __grid_constant__ CUtensorMap pool_map, const __grid_c
       }
     }
   } else if (warp >= 4) {
-    // ---- epilogue: two warpgroups take a segment's units in turn (the same
-    // one of them for every tile of a unit); thread i of a warpgroup owns
-    // token i of this CTA's half
+    // ---- epilogue: thread i of either warpgroup holds token i of this CTA's
+    // half; the first adds up the even groups of 32 columns, the second the
+    // odd ones
     const int i = (tid - 128) & 127, wg = warp >= 8 ? 1 : 0, wq = warp & 3;
     const uint32_t lane_off = uint32_t(wq * 32) << 16;
     const uint32_t d_empty0 = mapa(bar(bars->d_empty[0]), 0);
     float* nlse = reinterpret_cast<float*>(smem + kOffNlse);      // per column: -lse in log2 units
     float* cscale = nlse + 128;                                   // FP8: 2^e * scale
-    int* vis = reinterpret_cast<int*>(smem + kOffVis);            // per column: tokens it sees, 0 if it adds nothing
-    int* gmin = reinterpret_cast<int*>(smem + kOffGmin);          // of 32 columns
+    uint16_t* hid = reinterpret_cast<uint16_t*>(smem + kOffHid);  // per column: the last tokens that it does not see
+    int* gmin = reinterpret_cast<int*>(smem + kOffGmin);
     int* gmax = reinterpret_cast<int*>(smem + kOffGmax);
+    float* part = reinterpret_cast<float*>(smem + kOffPart);
     const int cap = a.max_pages * MLA_PAGE_SIZE;
-    uint32_t units = 0;   // before this segment
+    uint32_t n = 0;   // units so far
     // A warp whose wait failed says so at the group's next barrier, where all
-    // eight leave together.  The barrier at a segment's start also keeps the
-    // parity waits sound: every earlier unit has been drained, by whichever
-    // warpgroup, before one of this segment is waited for.
+    // eight leave together.
     bool ok = true, met = true;
     each_seg(a, plan, [&](const Seg& sg) {
-      if (!named_bar_and(kEpiBar, kEpiThreads, ok)) return met = false;
+      if (!named_bar_and(kEpiBar, kEpiThreads, ok)) return met = false;   // everyone is done with the last columns
       const int c = tid - 128;
       if (c < 2 * sg.nh) {
         const int row = sg.row0 + c;
         int v = 0;
+        uint16_t hd = kDead;
         float nl = 0.f, cs = 0.f;
         if (row < min(a.rows, sg.row0 + plan.tile)) {
           const float l = a.lse[size_t(sg.r) * a.rows + row];
           if (l != -INFINITY) {
             v = min(sg.t, visible_len(sg.t, a.s_q, row / a.heads, a.causal));
+            hd = uint16_t(sg.t - v < kDead ? sg.t - v : kDead);   // (sees nothing, or hides fewer than s_q <= 65534)
             nl = -l * 1.4426950408889634f;
           }
           if (kFp8) cs = a.q_scale[size_t(sg.r) * a.rows + row] * a.sl2;
         }
         nlse[c] = nl;
         if (kFp8) cscale[c] = cs;
-        vis[c] = v;
+        hid[c] = v > 0 ? hd : kDead;
         const int lo = __reduce_min_sync(0xffffffffu, v), hi = __reduce_max_sync(0xffffffffu, v);
         if (lane == 0) {
           gmin[c >> 5] = lo;
@@ -527,32 +536,31 @@ attn_weights_kernel(const __grid_constant__ CUtensorMap pool_map, const __grid_c
       const int ngroups = 2 * sg.nh / 32;
       const int32_t* bt = a.block_table + size_t(sg.r) * a.max_pages;
       const bool direct = plan.groups == 1;
-      const bool reads_old = direct ? !sg.first_tile || a.decay != 0.f : !sg.first;
+      const bool reads_old = wg == 0 && (direct ? !sg.first_tile || a.decay != 0.f : !sg.first);
       auto pos_of = [&](int u) { return u * kUnit + int(rank) * kHalf + i; };
-      auto sum_at = [&](int u) {   // where this thread's sum of unit u lives
+      auto sum_at = [&](int u) {   // where the token's sum of unit u lives
         return direct ? a.weights + size_t(sg.r) * cap + pos_of(u)
                       : a.partial + (size_t(sg.group) * a.max_units + sg.unit0 + u) * kUnit + (pos_of(u) - u * kUnit);
       };
       // page id (-2: no token here), token scale and old sum of a unit; the
-      // ids are read two of this warpgroup's units ahead, the rest one
+      // ids are read two units ahead, the rest one
       auto page_at = [&](int u) { return u < sg.u1 && pos_of(u) < sg.t ? bt[pos_of(u) / MLA_PAGE_SIZE] : -2; };
       auto scale_at = [&](int u, int page) {
         return kFp8 && page >= 0 && page < a.num_pages ? a.kv_scale[size_t(page) * MLA_PAGE_SIZE + pos_of(u) % MLA_PAGE_SIZE]
                                                        : 0.f;
       };
       auto old_at = [&](int u, int page) { return reads_old && page != -2 ? *sum_at(u) : 0.f; };
-      const int ua = sg.u0 + ((wg ^ sg.r) & 1);
-      int page = page_at(ua), page1 = page_at(ua + 2);
-      float stok = scale_at(ua, page), old = old_at(ua, page);
+      int page = page_at(sg.u0), page1 = page_at(sg.u0 + 1);
+      float stok = scale_at(sg.u0, page), old = old_at(sg.u0, page);
       if (!named_bar_and(kEpiBar, kEpiThreads, true)) return met = false;   // the columns are in place
-      for (int u = ua; u < sg.u1; u += 2) {
-        const int page2 = page_at(u + 4);
-        const float stok1 = scale_at(u + 2, page1), old1 = old_at(u + 2, page1);
-        const uint32_t n = units + uint32_t(u - sg.u0), buf = n & 1u, d = tmem + lane_off + 256u * buf;
+      for (int u = sg.u0; u < sg.u1; ++u, ++n) {
+        const int page2 = page_at(u + 2);
+        const float stok1 = scale_at(u + 1, page1), old1 = old_at(u + 1, page1);
+        const uint32_t buf = n & 1u, par = (n >> 1) & 1u, d = tmem + lane_off + 256u * buf;
         const int pos0 = u * kUnit + int(rank) * kHalf, pos = pos0 + i;
         const bool live = page != -2, good = page >= 0 && page < a.num_pages;
         const int top = min(sg.t, pos0 + kHalf) - 1;   // the half's last token
-        if (!w_warp_wait(ctl, bar(bars->d_full[buf]), (n >> 1) & 1u)) {
+        if (!w_warp_wait(ctl, bar(bars->d_full[buf]), par)) {
           ok = false;
           break;
         }
@@ -560,7 +568,7 @@ attn_weights_kernel(const __grid_constant__ CUtensorMap pool_map, const __grid_c
         float s0 = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
         if (top >= pos0) {
 #pragma unroll 1
-          for (int g = 0; g < ngroups; ++g) {
+          for (int g = wg; g < ngroups; g += 2) {
             if (pos0 >= gmax[g]) continue;   // no column of the group sees a token of this half
             uint32_t x[32];
             tmem_ld32(d + 32u * uint32_t(g), x);
@@ -598,43 +606,63 @@ attn_weights_kernel(const __grid_constant__ CUtensorMap pool_map, const __grid_c
                 s3 += ex2(v[k + 3]);
               }
             } else {
+              const int behind = sg.t - pos;   // tokens from this one to the end (a column that hides fewer sees it)
 #pragma unroll
               for (int k = 0; k < 32; k += 4) {
-                const int4 w = *reinterpret_cast<const int4*>(vis + 32 * g + k);
-                s0 += pos < w.x ? ex2(v[k]) : 0.f;
-                s1 += pos < w.y ? ex2(v[k + 1]) : 0.f;
-                s2 += pos < w.z ? ex2(v[k + 2]) : 0.f;
-                s3 += pos < w.w ? ex2(v[k + 3]) : 0.f;
+                const ushort4 h = *reinterpret_cast<const ushort4*>(hid + 32 * g + k);
+                s0 += h.x != kDead && int(h.x) < behind ? ex2(v[k]) : 0.f;
+                s1 += h.y != kDead && int(h.y) < behind ? ex2(v[k + 1]) : 0.f;
+                s2 += h.z != kDead && int(h.z) < behind ? ex2(v[k + 2]) : 0.f;
+                s3 += h.w != kDead && int(h.w) < behind ? ex2(v[k + 3]) : 0.f;
               }
             }
           }
         }
         tc_fence_before();
-        __syncwarp();
-        if (lane == 0) arrive_first(d_empty0 + 8u * buf);
-        const float sum = good ? (s0 + s1) + (s2 + s3) : 0.f;
-        if (live) {
-          if (!good) flag_status(a.ws, kStatusBadPage);
-          *sum_at(u) = fmaf(direct && sg.first_tile ? a.decay : 1.f, old, sum);
-        }
-        if (!direct && sg.last) {
-          // the group's sums of this unit are in: whichever warp is the last
-          // of the groups to say so adds its 32 tokens' sums up, in the
-          // groups' order
-          __threadfence();
+        float sum = (s0 + s1) + (s2 + s3);
+        if (wg == 1) {
+          // hand the odd groups' sum over; the first warpgroup frees the
+          // accumulator only once it has it, so this place is free again
+          // before the accumulator's next unit
+          part[128 * buf + i] = sum;
           __syncwarp();
-          uint32_t done = 0;
-          if (lane == 0) done = atomicAdd(a.counters + 8 * size_t(sg.unit0 + u) + 4 * rank + wq, 1u);
-          done = __shfl_sync(0xffffffffu, done, 0);
-          if (done == uint32_t(plan.groups - 1)) {
+          if (lane == 0) {
+            mbar_arrive(bar(bars->part_full[buf]));
+            arrive_first(d_empty0 + 8u * buf);
+          }
+        } else {
+          if (!w_warp_wait(ctl, bar(bars->part_full[buf]), par)) {
+            ok = false;
+            break;
+          }
+          sum += part[128 * buf + i];
+          __syncwarp();
+          if (lane == 0) arrive_first(d_empty0 + 8u * buf);
+          if (!good) sum = 0.f;
+          if (live) {
+            if (!good) flag_status(a.ws, kStatusBadPage);
+            *sum_at(u) = fmaf(direct && sg.first_tile ? a.decay : 1.f, old, sum);
+          }
+          if (!direct && sg.last) {
+            // the group's sums of this unit are in: whichever warp is the
+            // last of the groups to say so adds its 32 tokens' sums up, in
+            // the groups' order
             __threadfence();
-            if (lane == 0) a.counters[8 * size_t(sg.unit0 + u) + 4 * rank + wq] = 0u;
-            if (live) {
-              float* w = a.weights + size_t(sg.r) * cap + pos;
-              float s = a.decay != 0.f ? a.decay * *w : 0.f;
-              const float* part = a.partial + size_t(sg.unit0 + u) * kUnit + (pos - u * kUnit);
-              for (int k = 0; k < plan.groups; ++k) s += __ldcg(part + size_t(k) * a.max_units * kUnit);
-              *w = s;
+            __syncwarp();
+            uint32_t* count = a.counters + 8 * size_t(sg.unit0 + u) + 4 * rank + wq;
+            uint32_t done = 0;
+            if (lane == 0) done = atomicAdd(count, 1u);
+            done = __shfl_sync(0xffffffffu, done, 0);
+            if (done == uint32_t(plan.groups - 1)) {
+              __threadfence();
+              if (lane == 0) *count = 0u;
+              if (live) {
+                float* w = a.weights + size_t(sg.r) * cap + pos;
+                float s = a.decay != 0.f ? a.decay * *w : 0.f;
+                const float* from = a.partial + size_t(sg.unit0 + u) * kUnit + (pos - u * kUnit);
+                for (int k = 0; k < plan.groups; ++k) s += __ldcg(from + size_t(k) * a.max_units * kUnit);
+                *w = s;
+              }
             }
           }
         }
@@ -643,7 +671,6 @@ attn_weights_kernel(const __grid_constant__ CUtensorMap pool_map, const __grid_c
         stok = stok1;
         old = old1;
       }
-      units += uint32_t(sg.u1 - sg.u0);
       return true;
     });
     if (met) named_bar_and(kEpiBar, kEpiThreads, ok);

@@ -69,6 +69,8 @@ def test_attn_weights_argument_checks():
                dict(sh=shape(cache_dtype="fp8"))):
         assert call(**kw) == -1, kw
     assert call(sh=shape(batch=65536, s_q=1, num_heads=1)) == -2
+    assert call(sh=shape(batch=1, s_q=65535, num_heads=1)) == -2
+    assert L.mla_attn_weights_workspace_bytes(ctypes.byref(shape(batch=1, s_q=65535, num_heads=1)), 148) == 0
     assert L.mla_attn_weights_workspace_bytes(ctypes.byref(shape()), 148) >= 256
     assert L.mla_attn_weights_workspace_bytes(ctypes.byref(shape()), 0) == 0
     assert L.mla_attn_weights_workspace_bytes(ctypes.byref(shape(batch=65536, s_q=1, num_heads=1)), 148) == 0
