@@ -285,7 +285,8 @@ int mla_var6_get_device_status(const mla_shape_t* shape, int n_new, int num_sms,
  *               outside [0, min(s_q, t)] is clamped and flagged.
  *   tree_mask : device int64 [batch, s_q, ceil(s_q / 64)], 8-byte aligned.
  *   q, kv_cache, kv_scale, block_table, seqlens, softmax_scale, out, lse: as
- *               for mla_decode_fwd, with its condition on the value rows.
+ *               for mla_decode_fwd, with its condition on the value rows of
+ *               every position before t, seen by a node or not.
  *   workspace : mla_tree_workspace_bytes(shape, num_sms of this device)
  *               bytes, 256-byte aligned, zero-filled before its first use (it
  *               holds the schedule and the status word); the caller must not
@@ -351,7 +352,8 @@ int mla_attn_weights_get_device_status(void* workspace, void* stream, int* statu
  *   max_tokens: row length of weights; seqlens outside [0, max_tokens] are
  *             clamped and flagged.
  *   weights : fp32 [batch, max_tokens]; entries from seqlens[r] on not read.
- *   budget >= 1, sink >= 0, recent >= 0, sink + recent <= budget.
+ *   budget >= 1, sink >= 0, recent >= 0, sink + recent <= budget; batch <=
+ *             2^24, max_tokens and budget <= 2^30.
  *   kept    : int32 [batch, budget], the kept positions in ascending order,
  *             then -1 (the form of mla_sparse_decode_fwd's lists).
  *   kept_lens: int32 [batch], min(seqlens[r], budget).

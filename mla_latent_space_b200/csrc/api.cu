@@ -597,7 +597,7 @@ int mla_evict_select(int32_t batch, int32_t max_tokens, const float* weights, co
   CallRange range_("mla_evict_select");
   if (batch < 1 || max_tokens < 1 || budget < 1 || sink < 0 || recent < 0) return MLA_ERR_INVALID_ARG;
   if (int64_t(sink) + recent > budget) return MLA_ERR_INVALID_ARG;
-  if (max_tokens > (1 << 30) || budget > (1 << 30)) return MLA_ERR_UNSUPPORTED;
+  if (max_tokens > (1 << 30) || budget > (1 << 30) || batch > (1 << 24)) return MLA_ERR_UNSUPPORTED;
   if (!weights || !seqlens || !kept || !kept_lens) return MLA_ERR_INVALID_ARG;
   if (!aligned(weights, 4) || !aligned(seqlens, 4) || !aligned(kept, 4) || !aligned(kept_lens, 4) ||
       !aligned(device_status, 4))

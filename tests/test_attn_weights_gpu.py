@@ -170,8 +170,9 @@ def test_bad_lengths_and_pages_are_flagged_and_receive_nothing():
     assert run(wl, lse, 0.5, old, dev=dev)[1] == -6
 
 
-def test_two_calls_at_once_and_a_replayed_graph():
-    wl = mw.make(4, 2, 64, [3000, 500, 64, 1], seed=90)
+@pytest.mark.parametrize("cache", ["bf16", "fp8"])
+def test_two_calls_at_once_and_a_replayed_graph(cache):
+    wl = mw.make(4, 2, 64, [3000, 500, 64, 1], seed=90, cache_dtype=cache)
     lse, old = lse_of(wl), old_weights(wl)
     dev, accs = to_device(wl), [mla.AttnWeights(shape_of(wl)) for _ in range(2)]
     one, _ = run(wl, lse, 0.9, old, accs[0], dev)
@@ -181,7 +182,7 @@ def test_two_calls_at_once_and_a_replayed_graph():
     torch.cuda.synchronize()
     for _ in range(3):
         for acc, w, s in zip(accs, ws, streams):
-            acc.accumulate(*args, w, stream=s)
+            acc.accumulate(*args, w, kv_scale=dev["kv_scale"], stream=s)
     torch.cuda.synchronize()
     two = [w.cpu().numpy() for w in ws]
     seq = old
@@ -190,7 +191,7 @@ def test_two_calls_at_once_and_a_replayed_graph():
     assert np.array_equal(two[0], seq) and np.array_equal(two[1], seq)
     g = torch.cuda.CUDAGraph()
     with torch.cuda.graph(g):
-        accs[0].accumulate(*args, ws[0])
+        accs[0].accumulate(*args, ws[0], kv_scale=dev["kv_scale"])
     ws[0].copy_(torch.from_numpy(old))
     g.replay()
     torch.cuda.synchronize()
@@ -202,6 +203,19 @@ def test_two_calls_at_once_and_a_replayed_graph():
     torch.cuda.synchronize()
     got = ws[0].cpu().numpy()
     assert np.array_equal(got[0, 1234:], old[0, 1234:]) and np.array_equal(got[:, :1234], one[:, :1234])
+
+
+def test_infinite_lse_and_empty_batches():
+    # lse = +inf is a weight of zero; a batch without tokens is no work
+    wl = mw.make(2, 1, 16, [100, 70], seed=93)
+    lse, old = lse_of(wl), old_weights(wl)
+    lse[1] = np.inf
+    got, st = run(wl, lse, 0.5, old)
+    assert st == 0 and np.array_equal(got[1, :70], np.float32(0.5) * old[1, :70])
+    dev = to_device(wl)
+    dev["seqlens"].zero_()
+    got, st = run(wl, lse, 0.5, old, dev=dev)
+    assert st == 0 and np.array_equal(got, old)
 
 
 def test_binding_checks():

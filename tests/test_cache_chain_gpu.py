@@ -97,3 +97,41 @@ def test_draft_verify_accept_weigh_evict_decode(cache):
     assert_parity(compare(out1.float().cpu().numpy(), lse1.cpu().numpy(), O_ref, L_ref), "dense after eviction")
     assert_parity(compare(out_s.float().cpu().numpy(), lse_s.cpu().numpy(), O_ref, L_ref), "sparse before eviction")
     assert np.array_equal(w.cpu().numpy(), w_ref)
+
+
+@pytest.mark.parametrize("cache", ["bf16", "fp8"])
+def test_pools_past_four_gigabytes(cache):
+    # the workload's pages lie past the 2^32nd byte of the pool
+    wl = mw.make(2, 4, 16, [300, 130], seed=101, cache_dtype=cache)
+    far = (5 << 30) // (73728 if cache == "bf16" else 40960)
+    pages = far + wl.num_pages
+    pool = torch.zeros((pages,) + tuple(wl.pool.shape[1:]), dtype=wl.pool.dtype, device="cuda")
+    pool[far:] = wl.pool.cuda()
+    sc = None
+    if wl.kv_scale is not None:
+        sc = torch.ones((pages, 64), device="cuda")
+        sc[far:] = wl.kv_scale.cuda()
+    bt, sl, q = torch.from_numpy(wl.block_table + far).cuda(), torch.from_numpy(wl.seqlens).cuda(), wl.q.cuda()
+    shape = mla.make_shape(2, 4, 16, wl.max_pages, pages, cache)
+    mask = oracle.tree_mask(np.tile(np.array([-1, 0, 0, 1], dtype=np.int32), (2, 1)))
+    out = torch.empty((2, 4, 16, 512), dtype=torch.bfloat16, device="cuda")
+    lse = torch.empty((2, 4, 16), dtype=torch.float32, device="cuda")
+    tree = mla.TreeDecoder(shape)
+    tree.decode(q, pool, bt, sl, torch.from_numpy(mask).cuda(), wl.softmax_scale, out, lse, kv_scale=sc)
+    O_ref, L_ref = oracle.tree_decode(wl, mask)
+    assert_parity(compare(out.float().cpu().numpy(), lse.cpu().numpy(), O_ref, L_ref), "far tree")
+    l_ref = oracle.decode(wl)[1].astype(np.float32)
+    w = torch.zeros((2, wl.max_pages * 64), device="cuda")
+    acc = mla.AttnWeights(shape)
+    acc.accumulate(q, pool, bt, sl, torch.from_numpy(l_ref).cuda(), wl.softmax_scale, 0.0, w, kv_scale=sc)
+    ref = oracle.attn_weights(wl, l_ref, 0.0, np.zeros((2, wl.max_pages * 64)))
+    assert (np.abs(w.cpu().numpy() - ref) <= 5e-4 * ref).all()
+    src = np.stack([np.arange(3, 103), np.arange(30, 130)]).astype(np.int32)
+    comp = mla.CacheCompactor(shape, 100)
+    comp.compact(pool, bt, torch.from_numpy(src).cuda(), torch.tensor([100, 100], dtype=torch.int32, device="cuda"), kv_scale=sc)
+    p_ref, s_ref, _ = oracle.compact(wl.pool, wl.kv_scale, wl.block_table, src, [100, 100])
+    bits = lambda t: t.view(torch.int16) if t.dtype == torch.bfloat16 else t
+    assert torch.equal(bits(pool[far:].cpu()), bits(p_ref)) and not pool[:far].any()
+    if sc is not None:
+        assert torch.equal(sc[far:].cpu(), s_ref)
+    assert tree.status() == 0 and acc.status() == 0 and comp.status() == 0

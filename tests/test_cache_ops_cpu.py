@@ -91,6 +91,7 @@ def test_evict_select_argument_checks():
         assert call(**kw) == -1, kw
     assert call(T=(1 << 30) + 1) == -2
     assert call(budget=(1 << 30) + 1) == -2
+    assert call(b=(1 << 24) + 1) == -2
 
 
 def test_compact_argument_checks():

@@ -95,6 +95,30 @@ def test_select_does_not_read_behind_the_length_and_flags_bad_lengths():
     assert np.array_equal(k2, k_ref) and np.array_equal(l2, l_ref)
 
 
+def test_select_replays_from_a_graph_and_runs_on_two_streams():
+    for T in (3000, 20000):                                             # one CTA a request, and a cluster
+        ws = [weights(3, T, 60 + k) for k in range(3)]
+        dev = torch.from_numpy(ws[0]).cuda()
+        sl = torch.tensor([T, T // 2, 100], dtype=torch.int32, device="cuda")
+        kept = [torch.empty((3, 500), dtype=torch.int32, device="cuda") for _ in range(2)]
+        lens = [torch.empty(3, dtype=torch.int32, device="cuda") for _ in range(2)]
+        streams = [torch.cuda.Stream() for _ in range(2)]
+        torch.cuda.synchronize()
+        for k, s in zip(range(2), streams):
+            mla.mla_evict_select(dev, sl, 500, 4, 64, kept[k], lens[k], stream=s)
+        torch.cuda.synchronize()
+        ref = oracle.evict_select(ws[0], [T, T // 2, 100], 500, 4, 64)
+        assert all(np.array_equal(kept[k].cpu().numpy(), ref[0]) and np.array_equal(lens[k].cpu().numpy(), ref[1]) for k in range(2))
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            mla.mla_evict_select(dev, sl, 500, 4, 64, kept[0], lens[0])
+        for w in ws[1:]:
+            dev.copy_(torch.from_numpy(w))
+            g.replay()
+            torch.cuda.synchronize()
+            assert np.array_equal(kept[0].cpu().numpy(), oracle.evict_select(w, [T, T // 2, 100], 500, 4, 64)[0])
+
+
 # ---- compaction -----------------------------------------------------------------
 
 def lists(seqlens, rows, seed, base=None):
@@ -173,6 +197,17 @@ def test_compact_many_requests_again_and_again_through_one_workspace():
     for seed in range(4):
         src, lens = lists(seqlens, 700, seed=seed)
         check_compact(wl, src, lens, comp=comp)
+
+
+def test_compact_with_a_shared_prefix_that_stays():
+    # two requests list the same first pages; nothing moves there
+    wl = mw.make(2, 1, 1, [1000, 900], seed=18)
+    wl.block_table[1, :3] = wl.block_table[0, :3]
+    src = np.full((2, 600), -1, dtype=np.int32)
+    for r, t in enumerate((1000, 900)):
+        src[r, :192] = np.arange(192)
+        src[r, 192:600] = 192 + np.sort(np.random.default_rng(r).permutation(t - 192)[:408])
+    check_compact(wl, src, np.array([600, 600], dtype=np.int32))
 
 
 def test_compact_flags_bad_lists_and_touches_no_other_request():

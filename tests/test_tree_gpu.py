@@ -116,6 +116,33 @@ def test_ragged_trees_no_tree_no_tokens_and_rows_that_see_nothing(cache):
     assert np.isneginf(L[2, 0]).all() and (O[2, 0] == 0).all() and np.isneginf(L[0]).all() and np.isneginf(L[3, 9:]).all()
 
 
+def test_without_counts_a_short_request_holds_as_many_nodes_as_tokens():
+    wl = mw.make(3, 16, 40, [5, 16, 17], seed=74, name="short_tree")
+    O, L = check(wl, oracle.tree_mask(np.tile(np.arange(-1, 15, dtype=np.int32), (3, 1))))
+    assert np.isneginf(L[0, 5:]).all() and np.isfinite(L[0, :5]).all()
+
+
+def test_two_calls_at_once_on_two_streams():
+    wl = mw.make(3, 8, 64, [900, 65, 2000], seed=75)
+    dev = to_device(wl)
+    masks = [oracle.tree_mask(parents_of(3, 8, seed=s)) for s in (76, 77)]
+    decs = [mla.TreeDecoder(shape_of(wl)) for _ in masks]
+    md = [torch.from_numpy(m).cuda() for m in masks]
+    outs = [torch.empty((3, 8, 64, 512), dtype=torch.bfloat16, device="cuda") for _ in masks]
+    lses = [torch.empty((3, 8, 64), dtype=torch.float32, device="cuda") for _ in masks]
+    streams = [torch.cuda.Stream() for _ in masks]
+    torch.cuda.synchronize()
+    for _ in range(4):
+        for k in range(2):
+            decs[k].decode(dev["q"], dev["pool"], dev["block_table"], dev["seqlens"], md[k], wl.softmax_scale, outs[k],
+                           lses[k], stream=streams[k])
+    torch.cuda.synchronize()
+    for k in range(2):
+        assert decs[k].status() == 0
+        O_ref, L_ref = oracle.tree_decode(wl, masks[k])
+        assert_parity(compare(outs[k].float().cpu().numpy(), lses[k].cpu().numpy(), O_ref, L_ref), f"stream {k}")
+
+
 def test_nodes_behind_the_last_page_are_not_read():
     # NaN behind every length and in RoPE columns of a node that nobody sees: no trace in the output
     wl = mw.make(2, 12, 128, [100, 75], seed=65, name="poison")
