@@ -76,18 +76,20 @@ __device__ __forceinline__ void st_release(uint32_t* p, uint32_t v) {
   asm volatile("st.release.gpu.global.u32 [%0], %1;" ::"l"(p), "r"(v) : "memory");
 }
 
-// Index of the first of the ascending src[0..n) that is >= x (n if none), by
-// one warp in steps of 32 (256 threads a step would read 8 KB of list for
-// every 36 KB of rows).
-__device__ __forceinline__ int first_at_least(const int32_t* src, int n, int x) {
-  int a = 0, b = n;
-  while (a < b) {
-    const int step = (b - a + 31) / 32;
-    const int64_t i = int64_t(a) + int64_t(threadIdx.x & 31) * step;
-    const int c = __popc(__ballot_sync(0xffffffffu, i < b && src[i] < x));
+// Of the groups 0 .. n-1 of an ascending list, the last whose first entry is
+// below x (0 if none), by one warp, 64 groups a step.
+template <int kRows>
+__device__ __forceinline__ int group_below(const int32_t* src, int n, int x) {
+  const int lane = int(threadIdx.x & 31);
+  int a = 0, b = n;   // the answer is in [a, b), or 0
+  while (b - a > 1) {
+    const int step = (b - a + 63) / 64;
+    const int64_t i = int64_t(a) + int64_t(lane) * step, j = i + int64_t(32) * step;
+    const int c = __popc(__ballot_sync(0xffffffffu, i < b && src[i * kRows] < x)) +
+                  __popc(__ballot_sync(0xffffffffu, j < b && src[j * kRows] < x));
     if (c == 0) return a;
     b = int(min(int64_t(b), int64_t(a) + int64_t(c) * step));
-    a = a + (c - 1) * step + 1;
+    a = a + (c - 1) * step;
   }
   return a;
 }
@@ -96,30 +98,40 @@ template <bool kFp8>
 __global__ void __launch_bounds__(kCompThreads, kCompCtas) compact_kernel(const CompArgs a) {
   constexpr int kRows = kCompRows<kFp8>, kCh = kChunks<kFp8>, kPer = kRows * kCh / kCompThreads;
   static_assert(kRows * kCh % kCompThreads == 0 && kRows <= kCompThreads - 32, "pieces");
-  __shared__ int64_t from[2][kRows], to[2][kRows];
-  __shared__ int pos_from[2][kRows], pos_to[2][kRows];
-  __shared__ int first_sh[2];   // entries from here to the group's own may have their sources at its destinations
+  // three buffers: a group's rows are still being written when the one after
+  // the next is resolved
+  __shared__ int64_t from[3][kRows], to[3][kRows];
+  __shared__ int pos_from[3][kRows], pos_to[3][kRows];
+  __shared__ int needs[3];        // the first of the groups whose sources may lie at its destinations; the group itself: none
+  __shared__ int ready_sh[3];     // ... have been read already
   __shared__ uint32_t epoch_sh;
   const int tid = threadIdx.x;
   const bool solo = a.groups == 1;   // no other group's rows to wait for
   const uint32_t total = uint32_t(a.batch) * uint32_t(a.groups);
   const int cap = a.max_pages * MLA_PAGE_SIZE;
   bool bad = false;
+  int r_known = -1, n = 0, base = 0;   // request, its list's length and base
 
   // Resolves the rows of group `item` into buffer b; true where this
   // thread's row moves.  exists: whether the request's list reaches the group.
   auto resolve = [&](uint32_t item, int b, bool* exists) -> bool {
     const int r = int(item % uint32_t(a.batch)), g = int(item / uint32_t(a.batch));
-    int n = a.src_lens[r];
-    const int base = a.base != nullptr ? a.base[r] : 0;
-    if (g == 0 && (n < 0 || n > a.max_rows || base < 0)) bad = true;
-    n = base < 0 ? 0 : max(0, min(n, a.max_rows));
+    if (r != r_known) {
+      r_known = r;
+      n = a.src_lens[r];
+      base = a.base != nullptr ? a.base[r] : 0;
+      if (g == 0 && (n < 0 || n > a.max_rows || base < 0)) bad = true;
+      n = base < 0 ? 0 : max(0, min(n, a.max_rows));
+    }
     const int k0 = g * kRows;
     const int32_t* src = a.src + size_t(r) * a.max_rows;
     *exists = k0 < n;
     if (tid >= kCompThreads - 32) {   // the last warp resolves no rows
-      const int first = g == 0 || k0 >= n || int64_t(base) + k0 >= cap ? k0 : first_at_least(src, k0, base + k0);
-      if (tid == kCompThreads - 32) first_sh[b] = first;
+      // (src[k] >= base + k, so an earlier entry whose source is not before
+      // this group's destinations exists only where the last one's is not)
+      const bool none = g == 0 || k0 >= n || int64_t(base) + k0 >= cap || src[k0 - 1] < base + k0;
+      const int g0 = none ? g : group_below<kRows>(src, g, base + k0);
+      if (tid == kCompThreads - 32) needs[b] = g0;
     }
     if (tid >= kRows) return false;
     const int k = k0 + tid;
@@ -151,16 +163,19 @@ __global__ void __launch_bounds__(kCompThreads, kCompCtas) compact_kernel(const 
   bool exists = false;
   bool moves = __syncthreads_or(resolve(item, 0, &exists));   // (the grid has no CTA without an item)
   const uint32_t epoch = epoch_sh;
-  for (int b = 0; item < total; b ^= 1) {   // (uniform in the CTA)
+  int b = 0;
+  while (item < total) {   // (uniform in the CTA)
     const int r = int(item % uint32_t(a.batch)), g = int(item / uint32_t(a.batch));
     uint32_t* flags = a.ws + kStatusBytes / 4 + size_t(r) * a.groups;
     uint4 v[kPer];
     float sc = 0.f, w = 0.f;
     const bool mine = moves && tid < kRows && from[b][tid] >= 0;
+    uint32_t seen = 0;
     if (moves) {
 #pragma unroll
       for (int u = 0; u < kPer; ++u) {
         const int e = tid + kCompThreads * u, row = e / kCh;
+        v[u] = make_uint4(0, 0, 0, 0);
         if (from[b][row] >= 0)
           v[u] = __ldcg(reinterpret_cast<const uint4*>(a.kv + piece_offset<kFp8>(from[b][row], e % kCh)));
       }
@@ -169,20 +184,35 @@ __global__ void __launch_bounds__(kCompThreads, kCompCtas) compact_kernel(const 
         if (a.weights != nullptr) w = __ldcg(a.weights + size_t(r) * cap + pos_from[b][tid]);
       }
     }
-    // while they are on their way: the next group
+    // while they are on their way: whether the groups to wait for have been
+    // read, and the next group
+    const int g0 = needs[b], g1 = min(g0 + 1, g - 1);   // two at most: kRows places hold sources of kRows entries in a row
+    const bool waits = moves && !solo && g0 < g;
+    if (waits && tid < 2) {
+      const bool ok = g0 + tid > g1 || ld_acquire(flags + g0 + tid) == epoch;
+      const bool both = __all_sync(3u, ok);
+      if (tid == 0) ready_sh[b] = both;
+    }
     const uint32_t next = item + gridDim.x;   // (below 2^32: both are below 2^31)
+    const int bn = b == 2 ? 0 : b + 1;
     bool next_exists = false, next_moves = false;
-    if (next < total) next_moves = resolve(next, b ^ 1, &next_exists);
-    __threadfence();                                   // this thread's rows have been read ...
-    next_moves = __syncthreads_or(next_moves) != 0;    // ... and the CTA's
+    if (next < total) next_moves = resolve(next, bn, &next_exists);
+    // This thread's rows have been read once something has used them; `zero`
+    // is a zero that the compiler does not know.  (A fence would also wait
+    // for the last group's stores.)
+    if (moves) {
+#pragma unroll
+      for (int u = 0; u < kPer; ++u) seen |= v[u].x;
+      seen |= __float_as_uint(sc) | __float_as_uint(w);
+    }
+    uint32_t zero = uint32_t(a.batch) >> 31;
+    asm volatile("and.b32 %0, %0, %1;" : "+r"(zero) : "r"(seen));
+    next_moves = __syncthreads_or(next_moves || zero != 0u) != 0;   // the CTA's rows have been read
     bool ok = true;
     if (exists && !solo) {
       if (tid == 0) st_release(flags + g, epoch);
-      const int first = first_sh[b];
-      if (moves && first < g * kRows) {
-        // the groups whose sources are this group's destinations: two at most
-        const int g0 = first / kRows, g1 = (min(first + kRows, g * kRows) - 1) / kRows;
-        if (tid <= g1 - g0 && ld_acquire(flags + g0 + tid) != epoch) {
+      if (waits && !ready_sh[b]) {
+        if (tid <= g1 - g0) {
           uint64_t t0, t1;
           asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t0));
           while (ld_acquire(flags + g0 + tid) != epoch) {
@@ -212,7 +242,7 @@ __global__ void __launch_bounds__(kCompThreads, kCompCtas) compact_kernel(const 
     item = next;
     exists = next_exists;
     moves = next_moves;
-    __syncthreads();   // buffer b is filled again in the next turn
+    b = bn;
   }
   if (bad) atomicOr(reinterpret_cast<int32_t*>(a.ws), kStatusBadInput);
   if (!solo && tid == 0 && atomicAdd(a.ws + C_DONE, 1u) == gridDim.x - 1) {
@@ -241,8 +271,11 @@ int launch_compact(const mla_shape_t* shape, void* kv, float* kv_scale, const in
   const int groups = groups_for(fp8, max_rows);
   CompArgs a{static_cast<uint8_t*>(kv), kv_scale, block_table, src, src_lens, base, weights, static_cast<uint32_t*>(ws),
              shape->batch, groups, max_rows, shape->max_pages_per_seq, shape->num_pages};
-  // as many CTAs as are resident; where no CTA waits for another, one each
-  const int64_t total = int64_t(shape->batch) * groups, resident = kCompCtas * int64_t(num_sms);
+  // as many CTAs as are resident, in whole rounds of the requests (a CTA then
+  // stays with one); where no CTA waits for another, one each
+  const int64_t total = int64_t(shape->batch) * groups;
+  int64_t resident = kCompCtas * int64_t(num_sms);
+  if (shape->batch < resident) resident -= resident % shape->batch;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(unsigned(groups == 1 || total < resident ? total : resident));
   cfg.blockDim = dim3(kCompThreads);
