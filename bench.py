@@ -42,15 +42,15 @@ L2_FLUSH_BYTES = 256 << 20
 # for the kernel sources they were taken on: reported as null as soon as any
 # of them differs (checked by content hash at run time).
 TRAFFIC_SOURCES_SHA1 = {
-    "mla_latent_space_b200/csrc/decode_sm100.cu": "183aaa293124ca5522473db1c40c5912bbf84146",
+    "mla_latent_space_b200/csrc/decode_sm100.cu": "a976802f90c8fc308dccae0376c067f93463965c",
     "mla_latent_space_b200/csrc/sm100_ptx.cuh": "a666c6fb95adecc45850f281b1be3ecacba5d16c",
-    "mla_latent_space_b200/csrc/kernel_util.cuh": "9d7c3e48c90d2d444145ab84159f8400e402f999",
-    "mla_latent_space_b200/csrc/common.cuh": "7c6e8d72ef32d67aafb386e65a6767fa77f51a7f",
-    "mla_latent_space_b200/csrc/decode_launch.cuh": "627872ce2ed746bf011fb893a4fd1851f41ed788",
+    "mla_latent_space_b200/csrc/kernel_util.cuh": "b3f72c3cb1f09be8899208755a3eda87bfb3c5d1",
+    "mla_latent_space_b200/csrc/common.cuh": "112e1e06f7ebdafd951c11882ff99bebf48144d8",
+    "mla_latent_space_b200/csrc/decode_launch.cuh": "e64bf743c78208194d85090d84f93c37d7a51217",
 }
 TRAFFIC_BYTES = {
-    "dsv3_b64_h128_t4096_paged": 311544064 + 4859648,
-    "fp8_b64_h128_t32768": 1374417664 + 22606336,
+    "dsv3_b64_h128_t4096_paged": 311557376 + 4494848,
+    "fp8_b64_h128_t32768": 1375024128 + 22730752,
 }
 
 

@@ -1109,8 +1109,6 @@ decode_sm100_kernel(const __grid_constant__ CUtensorMap pool_map, const __grid_c
       uint32_t ne = 0;
       each_piece(sv, [&](const Piece& pc) {
         const int r = pc.T / sv.tiles_per_req, qt = pc.T % sv.tiles_per_req;
-        const int rho = qt * MLA_TILE_ROWS + i;
-        const bool valid = rho < rows_total;
         for (;;) {
           if (!wwait(ctl, bar(bars->corr_go), ne & 1u)) return false;
           ++ne;
