@@ -233,8 +233,14 @@ struct TreeLayout {
   size_t sched, sched_bytes, ws, ws_bytes, total;
 };
 
+int tree_overhead(const mla_shape_t* s) {
+  return s->cache_dtype == MLA_CACHE_FP8_E4M3 ? kTreeOverheadFp8 : kTreeOverhead;
+}
+
 bool tree_layout(const mla_shape_t* s, int num_sms, TreeLayout* L) {
   if (check_shape(s) != MLA_OK || s->causal != 0 || num_sms < 1) return false;
+  const ShapeInfo si = shape_info(s);
+  if (int64_t(si.batch) * si.tiles_per_req * (int64_t(si.max_pages) + tree_overhead(s)) >= (int64_t(1) << 31)) return false;
   L->sched = 0;
   L->sched_bytes = sched_bytes_for(s, num_sms);
   L->ws = (L->sched_bytes + 255) & ~size_t(255);
@@ -544,6 +550,7 @@ int mla_tree_decode_fwd(const mla_shape_t* shape, const void* q, const void* kv_
   ShapeInfo si = shape_info(shape);
   si.tree = 1;
   si.draft_lens = draft_lens;
+  si.overhead = tree_overhead(shape);
   if (launch_schedule(seqlens, si, num_workers_for(sms), static_cast<int32_t*>(sched), st) != cudaSuccess)
     return MLA_ERR_CUDA;
   const TreeArgs tree{draft_lens, tree_mask, (shape->s_q + 63) / 64};

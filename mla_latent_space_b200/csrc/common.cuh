@@ -29,6 +29,12 @@ constexpr int32_t kSchedMagic = 0x4d4c4131;  // "MLA1"
 // Cost of one piece beyond its pages, in page units: loading the 128x576
 // query tile and writing the 128x512 result cost about as much as two pages.
 constexpr int kPieceOverhead = 2;
+// The tree decode's, as measured: a piece's start and end cost more than that
+// beside a page's 1.4 us (BF16) or 0.8 us (FP8).  With 2, 6 and 8 pages a
+// batch of 32 trees of 24 nodes and 16 heads over up to 8192 tokens took 106,
+// 100 and 100 us with a BF16 cache; with 2, 8, 12, 16 and 24 it took 188, 160,
+// 150, 150 and 160 us with FP8.
+constexpr int kTreeOverhead = 6, kTreeOverheadFp8 = 14;
 
 enum HeaderField {
   H_MAGIC = 0, H_WORKERS, H_TILES, H_TILES_PER_REQ, H_TOTAL_COST, H_MAX_SLOTS, H_STATUS,
@@ -62,6 +68,7 @@ struct ShapeInfo {
   // which it holds draft_lens[r] (null: every slot that its length allows)
   int tree = 0;
   const int32_t* draft_lens = nullptr;
+  int overhead = kPieceOverhead;   // of a piece, in pages (tree decode: kTreeOverhead*)
 };
 
 // Nodes of request r's drafted tree: the last n of its t tokens.  A count
@@ -100,7 +107,7 @@ MLA_HD int request_tile_pages(const ShapeInfo& s, int r, int t, int qt, int32_t*
   return tile_pages(s, t, qt);
 }
 
-MLA_HD int tile_cost(int pages) { return pages > 0 ? pages + kPieceOverhead : 0; }
+MLA_HD int tile_cost(const ShapeInfo& s, int pages) { return pages > 0 ? pages + s.overhead : 0; }
 // Last index i in [0, n) with a[i*stride] <= x (a non-decreasing); -1 if none.
 MLA_HD int last_le(const int32_t* a, int stride, int n, int64_t x) {
   int lo = 0, hi = n;  // answer in [lo-1, hi-1]
@@ -121,6 +128,13 @@ MLA_HD int64_t tp_key(int tile, int page) { return (int64_t(tile) << 32) | uint3
 // 64-page tiles over 74 SM pairs run faster whole, 1 tile per worker, than
 // cut to the even share of 57 units.)
 constexpr int kSplitOverhead = 12;
+
+// The even share of `total` over We workers that the whole-tile assignment is
+// held against.  Tree decode: no worker costs less than one piece of a page.
+MLA_HD int64_t even_share(const ShapeInfo& s, int64_t total, int64_t We) {
+  const int64_t share = (total + We - 1) / We;
+  return s.tree && share <= s.overhead ? s.overhead + 1 : share;
+}
 
 // Whole-tile assignment: worker w of We takes the tiles whose cost prefix
 // lies in [total*w/We, total*(w+1)/We).  prefix[T*stride] is tile T's

@@ -4,7 +4,7 @@
 //
 // The work of a decode step is a list of 128-row tiles (request r, row block
 // qt), each walking ceil(visible/64) KV pages.  Costing every tile as
-// pages + kPieceOverhead and laying the tiles end to end gives a line of
+// pages + an overhead (ShapeInfo::overhead) and laying the tiles end to end gives a line of
 // total cost C; worker w takes the units whose cost position lies in
 // [C*w/W, C*(w+1)/W).  A position inside a tile's overhead maps to the start
 // of that tile, so no worker gets an empty piece of a tile.  A tile cut by k
@@ -35,9 +35,9 @@ MLA_HD int clamp_seqlen(int t, int max_pages, int32_t* flag) {
 }
 
 // (tile, page) where cost position x starts.
-MLA_HD void map_position(const int32_t* tiles, int num_tiles, int64_t x, int* tile, int* page) {
+MLA_HD void map_position(const ShapeInfo& s, const int32_t* tiles, int num_tiles, int64_t x, int* tile, int* page) {
   int T = last_le(tiles + T_PREFIX, kTileInts, num_tiles, x);
-  int64_t pg = x - int64_t(tiles[size_t(T) * kTileInts + T_PREFIX]) - kPieceOverhead;
+  int64_t pg = x - int64_t(tiles[size_t(T) * kTileInts + T_PREFIX]) - s.overhead;
   *tile = T;
   *page = pg > 0 ? int(pg) : 0;
 }
@@ -70,11 +70,11 @@ MLA_HD void fill_header(int32_t* hdr, const ShapeInfo& s, int W, int num_tiles) 
 // start positions floor(total*w/W_eff) are strictly increasing and an
 // interior page boundary is never shared by two workers; the remaining
 // workers start (and end) at (num_tiles, 0).
-MLA_HD void worker_start(const int32_t* tiles, int num_tiles, int64_t total, int w, int W,
+MLA_HD void worker_start(const ShapeInfo& s, const int32_t* tiles, int num_tiles, int64_t total, int w, int W,
                          int* tile, int* page) {
   const int64_t We = total < W ? total : W;
   if (w >= We) { *tile = num_tiles; *page = 0; return; }
-  map_position(tiles, num_tiles, total * w / We, tile, page);
+  map_position(s, tiles, num_tiles, total * w / We, tile, page);
 }
 
 // ---- device scheduler ------------------------------------------------------
@@ -173,7 +173,7 @@ schedule_kernel(const int32_t* __restrict__ seqlens, ShapeInfo s, int W, int32_t
     const int t = clamp_seqlen(seqlens[r], s.max_pages, &flag);
     const int pages = request_tile_pages(s, r, t, qt, &flag);
     pages_sm[T] = pages;
-    local += tile_cost(pages);
+    local += tile_cost(s, pages);
   }
   if (flag) atomicOr(&flag_sh, flag);
   int64_t excl;
@@ -182,7 +182,7 @@ schedule_kernel(const int32_t* __restrict__ seqlens, ShapeInfo s, int W, int32_t
     prefix_sm[T] = int32_t(excl);
     tiles[size_t(T) * kTileInts + T_PAGES] = pages_sm[T];
     tiles[size_t(T) * kTileInts + T_PREFIX] = int32_t(excl);
-    excl += tile_cost(pages_sm[T]);
+    excl += tile_cost(s, pages_sm[T]);
   }
   __syncthreads();
 
@@ -196,7 +196,7 @@ schedule_kernel(const int32_t* __restrict__ seqlens, ShapeInfo s, int W, int32_t
     mw = c > mw ? c : mw;
   }
   mw = block_max(mw, warp_tot);
-  const bool whole = We > 0 && mw <= (total + We - 1) / We + kSplitOverhead;
+  const bool whole = We > 0 && mw <= even_share(s, total, We) + kSplitOverhead;
   if (whole) {
     for (int w = tid; w < W; w += kSchedThreads) {
       int tb, te;
@@ -227,7 +227,7 @@ schedule_kernel(const int32_t* __restrict__ seqlens, ShapeInfo s, int W, int32_t
     if (w < We) {
       const int64_t x = total * w / We;
       tile = last_le(prefix_sm, 1, num_tiles, x);
-      const int64_t pg = x - int64_t(prefix_sm[tile]) - kPieceOverhead;
+      const int64_t pg = x - int64_t(prefix_sm[tile]) - s.overhead;
       page = pg > 0 ? int(pg) : 0;
     }
     wkey[w] = tp_key(tile, page);
@@ -288,7 +288,7 @@ MLA_HD void plan_schedule_seq(const int32_t* seqlens, const ShapeInfo& s, int W,
     int pages = request_tile_pages(s, r, t, qt, &flag);
     tiles[size_t(T) * kTileInts + T_PAGES] = pages;
     tiles[size_t(T) * kTileInts + T_PREFIX] = int32_t(total);
-    total += tile_cost(pages);
+    total += tile_cost(s, pages);
   }
   {
     const int64_t We = total < W ? total : W;
@@ -301,7 +301,7 @@ MLA_HD void plan_schedule_seq(const int32_t* seqlens, const ShapeInfo& s, int W,
                         prefix_at(prefix, kTileInts, num_tiles, total, tb);
       mw = c > mw ? c : mw;
     }
-    if (We > 0 && mw <= (total + We - 1) / We + kSplitOverhead) {
+    if (We > 0 && mw <= even_share(s, total, We) + kSplitOverhead) {
       for (int w = 0; w < W; ++w) {
         int tb, te;
         whole_tile_range(prefix, kTileInts, num_tiles, total, We, w, &tb, &te);
@@ -325,7 +325,7 @@ MLA_HD void plan_schedule_seq(const int32_t* seqlens, const ShapeInfo& s, int W,
   }
   for (int w = 0; w < W; ++w) {
     int tile, page;
-    worker_start(tiles, num_tiles, total, w, W, &tile, &page);
+    worker_start(s, tiles, num_tiles, total, w, W, &tile, &page);
     int32_t* wm = workers + size_t(w) * kWorkerInts;
     wm[W_TILE_BEGIN] = tile;
     wm[W_PAGE_BEGIN] = page;
@@ -412,7 +412,7 @@ schedule_whole_tiles_kernel(const int32_t* __restrict__ seqlens, ShapeInfo s, in
     const int r = T / s.tiles_per_req, qt = T % s.tiles_per_req;
     const int pages = tile_pages(s, clamp_seqlen(seqlens[r], s.max_pages, &flag), qt);
     pages_sm[T] = pages;
-    local += tile_cost(pages);
+    local += tile_cost(s, pages);
   }
   if (flag) atomicOr(&flag_sh, flag);
   int64_t excl;
@@ -424,7 +424,7 @@ schedule_whole_tiles_kernel(const int32_t* __restrict__ seqlens, ShapeInfo s, in
     tm[T_PREFIX] = int32_t(excl);
     tm[T_SPLITS] = pages_sm[T] > 0 ? 1 : 0;
     tm[T_SLOT_BASE] = 0;
-    excl += tile_cost(pages_sm[T]);
+    excl += tile_cost(s, pages_sm[T]);
   }
   __syncthreads();
 

@@ -92,6 +92,15 @@ def test_tree_decode_parity(cache, s, heads, lens_t):
     check(wl, oracle.tree_mask(parents_of(3, s, seed=61)))
 
 
+@pytest.mark.parametrize("cache", ["bf16", "fp8"])
+def test_jagged_batches_are_cut_and_joined(cache):
+    # tiles cut into many pieces, whole ones and empty ones side by side
+    lens_t = [6000, 64, 700, 1, 0, 2500, 130, 9000]
+    wl = mw.make(8, 6, 40, lens_t, seed=78, cache_dtype=cache, name="jagged_tree")
+    mask = oracle.tree_mask(parents_of(8, 6, seed=79))
+    check(wl, mask, [6, 6, 2, 1, 0, 0, 5, 4])
+
+
 def test_tree_of_a_chain_equals_the_causal_decode():
     wl = mw.make(2, 16, 128, [300, 4096], causal=True, seed=62, name="chain")
     mask = oracle.tree_mask(np.tile(np.arange(-1, 15, dtype=np.int32), (2, 1)))
