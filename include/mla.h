@@ -323,7 +323,9 @@ int mla_tree_mask(int32_t batch, int32_t s_q, const int32_t* parents, const int3
  * for j < seqlens[r]; later entries are left as they were.  Which positions
  * query token i sees is the shape's causal rule (mla_decode_fwd).  lse is the
  * decode's output for the same q, cache and scale.  A row whose lse is -inf
- * adds nothing, whatever its q holds (so padded query tokens can be marked).
+ * adds nothing, whatever its q holds (so padded query tokens can be marked;
+ * a tree's accepted nodes are weighed after the compaction, causal, with their
+ * rows at the end of the step's and the rows before them marked).
  * decay = 0 does not read the old weights.  The sums are fp32, in an order
  * that does not change from call to call.
  *   shape, q, kv_cache, kv_scale, block_table, seqlens, softmax_scale: as for

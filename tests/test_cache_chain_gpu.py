@@ -2,6 +2,8 @@
 the compaction in a row, as a serving loop runs them, on the GPU against the
 fp64 oracle.
 """
+import dataclasses
+
 import numpy as np
 import pytest
 import torch
@@ -55,6 +57,21 @@ def test_draft_verify_accept_weigh_evict_decode(cache):
     wl.pool, wl.kv_scale, _ = oracle.compact(wl.pool, wl.kv_scale, wl.block_table, src, n, base)
     wl.seqlens = (base + n).astype(np.int32)
     sl.copy_(torch.from_numpy(wl.seqlens))
+
+    # the accepted nodes' weights: their rows at the end of the step's, the others without an lse, in causal order
+    q_acc = torch.zeros_like(wl.q)
+    l_acc = np.full((b, s, h), -np.inf, dtype=np.float32)
+    for r, p in enumerate(paths):
+        q_acc[r, s - len(p):] = wl.q[r, p]
+        l_acc[r, s - len(p):] = lse[r].cpu().numpy()[p]
+    acc_wl = dataclasses.replace(wl, q=q_acc, causal=True)
+    w = torch.zeros((b, wl.max_pages * 64), device="cuda")
+    mla.AttnWeights(mla.make_shape(b, s, h, wl.max_pages, wl.num_pages, cache, True)).accumulate(
+        q_acc.cuda(), pool, bt, sl, torch.from_numpy(l_acc).cuda(), wl.softmax_scale, 0.0, w, kv_scale=sc)
+    ref = oracle.attn_weights(acc_wl, l_acc, 0.0, np.zeros((b, wl.max_pages * 64)))
+    assert (np.abs(w.cpu().numpy() - ref) <= 5e-4 * ref).all()
+    for r, p in enumerate(paths):                       # each row's weights sum to one, up to the decode's lse
+        assert abs(w[r].double().sum().item() - h * len(p)) <= 1.5e-3 * h * len(p)
 
     # the next token decodes over the closed-up cache and leaves its weights
     wl.q, wl.s_q = wl.q[:, :1].contiguous(), 1
