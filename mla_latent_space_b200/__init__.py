@@ -133,7 +133,7 @@ def _ptr(t: Optional[torch.Tensor]):
 
 def _stream(stream=None):
     # the raw handle of the current stream, without building a Stream object (2 us a call)
-    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()) if stream is None else stream.cuda_stream
+    return _stream_of(torch.cuda.current_device(), stream)
 
 
 def _check(rc: int, where: str):
@@ -154,11 +154,18 @@ def _need(t: torch.Tensor, name: str, dtype, shape=None):
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
 
 
-def _on_current_device(*tensors):
-    dev = torch.cuda.current_device()
-    for t in tensors:
-        if t is not None and t.get_device() != dev:
-            raise ValueError(f"every tensor must be on the current device (cuda:{dev}), got one on cuda:{t.get_device()}")
+def _need_here(dev: int, t: torch.Tensor, name: str, dtype, shape=None):
+    """_need, and that the tensor is on device `dev`, the current one: a call
+    launches there, on that device's stream."""
+    if isinstance(t, torch.Tensor) and t.get_device() == dev and t.dtype is dtype and t.is_contiguous() \
+            and (shape is None or t.shape == shape):
+        return
+    _need(t, name, dtype, shape)
+    raise ValueError(f"{name} must be on the current device (cuda:{dev}), got cuda:{t.get_device()}")
+
+
+def _stream_of(dev: int, stream):
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
 
 
 def num_sms(device=None) -> int:
@@ -206,6 +213,17 @@ def _check_decode_tensors(shape, q, kv_cache, kv_scale, block_table, seqlens, ou
         _need(out, "out", torch.bfloat16, (b, s, h, D_V))
     if lse is not None:
         _need(lse, "lse", torch.float32, (b, s, h))
+
+
+def _need_cache(dev, sh, kv_cache, kv_scale, block_table):
+    if sh.cache_dtype == MLA_CACHE_BF16:
+        _need_here(dev, kv_cache, "kv_cache", torch.bfloat16, (sh.num_pages, PAGE, D_QK))
+        if kv_scale is not None:
+            raise ValueError("kv_scale is only used with the fp8 cache")
+    else:
+        _need_here(dev, kv_cache, "kv_cache", torch.uint8, (sh.num_pages, FP8_PAGE_BYTES))
+        _need_here(dev, kv_scale, "kv_scale", torch.float32, (sh.num_pages, PAGE))
+    _need_here(dev, block_table, "block_table", torch.int32, (sh.batch, sh.max_pages_per_seq))
 
 
 def _decode_common(fn, where, shape, q, kv_cache, kv_scale, block_table, seqlens, softmax_scale, sched,
@@ -356,16 +374,21 @@ class TreeDecoder:
 
     def decode(self, q, kv_cache, block_table, seqlens, tree_mask, softmax_scale, out, lse, draft_lens=None,
                kv_scale=None, stream=None):
-        sh = self.shape
-        _check_decode_tensors(sh, q, kv_cache, kv_scale, block_table, seqlens, out, lse)
-        _need(tree_mask, "tree_mask", torch.int64, (sh.batch, sh.s_q, (sh.s_q + 63) // 64))
+        sh, dev = self.shape, torch.cuda.current_device()
+        b, s, h = sh.batch, sh.s_q, sh.num_heads
+        _need_here(dev, q, "q", torch.bfloat16, (b, s, h, D_QK))
+        _need_cache(dev, sh, kv_cache, kv_scale, block_table)
+        _need_here(dev, seqlens, "seqlens", torch.int32, (b,))
+        _need_here(dev, tree_mask, "tree_mask", torch.int64, (b, s, (s + 63) // 64))
+        _need_here(dev, out, "out", torch.bfloat16, (b, s, h, D_V))
+        _need_here(dev, lse, "lse", torch.float32, (b, s, h))
         if draft_lens is not None:
-            _need(draft_lens, "draft_lens", torch.int32, (sh.batch,))
-        _on_current_device(self.workspace, q, kv_cache, kv_scale, block_table, seqlens, tree_mask, out, lse, draft_lens)
+            _need_here(dev, draft_lens, "draft_lens", torch.int32, (b,))
+        _need_here(dev, self.workspace, "the decoder's workspace", torch.uint8)
         rc = lib().mla_tree_decode_fwd(ctypes.byref(sh), _ptr(q), _ptr(kv_cache), _ptr(kv_scale), _ptr(block_table),
                                        _ptr(seqlens), _ptr(draft_lens), _ptr(tree_mask), float(softmax_scale),
                                        _ptr(self.workspace), self.workspace.numel(), _ptr(out), _ptr(lse),
-                                       _stream(stream))
+                                       _stream_of(dev, stream))
         _check(rc, "mla_tree_decode_fwd")
 
     def status(self, stream=None) -> int:
@@ -379,18 +402,18 @@ def mla_tree_mask(parents, tree_mask, draft_lens=None, device_status: Optional[t
     """tree_mask int64 [b, s, ceil(s / 64)]: bit d % 64 of word d / 64 of row
     i says whether drafted node d is i or an ancestor of i, from parents int32
     [b, s] (-1: the committed prefix)."""
-    _need(parents, "parents", torch.int32)
+    dev = torch.cuda.current_device()
+    _need_here(dev, parents, "parents", torch.int32)
     if parents.dim() != 2:
         raise ValueError(f"parents must have shape [batch, s_q], got {tuple(parents.shape)}")
     b, s = parents.shape
-    _need(tree_mask, "tree_mask", torch.int64, (b, s, (s + 63) // 64))
+    _need_here(dev, tree_mask, "tree_mask", torch.int64, (b, s, (s + 63) // 64))
     if draft_lens is not None:
-        _need(draft_lens, "draft_lens", torch.int32, (b,))
+        _need_here(dev, draft_lens, "draft_lens", torch.int32, (b,))
     if device_status is not None:
-        _need(device_status, "device_status", torch.int32)
-    _on_current_device(parents, tree_mask, draft_lens, device_status)
+        _need_here(dev, device_status, "device_status", torch.int32)
     _check(lib().mla_tree_mask(b, s, _ptr(parents), _ptr(draft_lens), _ptr(tree_mask), _ptr(device_status),
-                               _stream(stream)), "mla_tree_mask")
+                               _stream_of(dev, stream)), "mla_tree_mask")
 
 
 class AttnWeights:
@@ -412,13 +435,17 @@ class AttnWeights:
         """weights[r, j] = decay * weights[r, j] + the attention weight that
         the rows of q give cached token j (lse: the decode's output).  weights
         fp32 [b, max_pages * 64], updated in place."""
-        sh = self.shape
-        _check_decode_tensors(sh, q, kv_cache, kv_scale, block_table, seqlens, None, lse)
-        _need(weights, "weights", torch.float32, (sh.batch, sh.max_pages_per_seq * PAGE))
-        _on_current_device(self.workspace, q, kv_cache, kv_scale, block_table, seqlens, lse, weights)
+        sh, dev = self.shape, torch.cuda.current_device()
+        b, s, h = sh.batch, sh.s_q, sh.num_heads
+        _need_here(dev, q, "q", torch.bfloat16, (b, s, h, D_QK))
+        _need_cache(dev, sh, kv_cache, kv_scale, block_table)
+        _need_here(dev, seqlens, "seqlens", torch.int32, (b,))
+        _need_here(dev, lse, "lse", torch.float32, (b, s, h))
+        _need_here(dev, weights, "weights", torch.float32, (b, sh.max_pages_per_seq * PAGE))
+        _need_here(dev, self.workspace, "the object's workspace", torch.uint8)
         rc = lib().mla_attn_weights_fwd(ctypes.byref(sh), _ptr(q), _ptr(kv_cache), _ptr(kv_scale), _ptr(block_table),
                                         _ptr(seqlens), _ptr(lse), float(softmax_scale), float(decay), _ptr(weights),
-                                        _ptr(self.workspace), self.workspace.numel(), _stream(stream))
+                                        _ptr(self.workspace), self.workspace.numel(), _stream_of(dev, stream))
         _check(rc, "mla_attn_weights_fwd")
 
     def status(self, stream=None) -> int:
@@ -433,18 +460,18 @@ def mla_evict_select(weights, seqlens, budget, sink, recent, kept, kept_lens,
     """kept int32 [b, budget]: the positions that stay (the first `sink`, the
     last `recent`, the heaviest between), ascending, then -1; kept_lens int32
     [b].  weights fp32 [b, max_tokens]."""
-    _need(weights, "weights", torch.float32)
+    dev = torch.cuda.current_device()
+    _need_here(dev, weights, "weights", torch.float32)
     if weights.dim() != 2:
         raise ValueError(f"weights must have shape [batch, max_tokens], got {tuple(weights.shape)}")
-    b = weights.shape[0]
-    _need(seqlens, "seqlens", torch.int32, (b,))
-    _need(kept, "kept", torch.int32, (b, int(budget)))
-    _need(kept_lens, "kept_lens", torch.int32, (b,))
+    b, max_tokens = weights.shape
+    _need_here(dev, seqlens, "seqlens", torch.int32, (b,))
+    _need_here(dev, kept, "kept", torch.int32, (b, int(budget)))
+    _need_here(dev, kept_lens, "kept_lens", torch.int32, (b,))
     if device_status is not None:
-        _need(device_status, "device_status", torch.int32)
-    _on_current_device(weights, seqlens, kept, kept_lens, device_status)
-    _check(lib().mla_evict_select(b, weights.shape[1], _ptr(weights), _ptr(seqlens), int(budget), int(sink), int(recent),
-                                  _ptr(kept), _ptr(kept_lens), _ptr(device_status), _stream(stream)),
+        _need_here(dev, device_status, "device_status", torch.int32)
+    _check(lib().mla_evict_select(b, max_tokens, _ptr(weights), _ptr(seqlens), int(budget), int(sink), int(recent),
+                                  _ptr(kept), _ptr(kept_lens), _ptr(device_status), _stream_of(dev, stream)),
            "mla_evict_select")
 
 
@@ -462,25 +489,18 @@ class CacheCompactor:
         self.workspace = torch.zeros(nb, dtype=torch.uint8, device=self.device)
 
     def compact(self, kv_cache, block_table, src, src_lens, base=None, kv_scale=None, weights=None, stream=None):
-        sh = self.shape
-        if sh.cache_dtype == MLA_CACHE_BF16:
-            _need(kv_cache, "kv_cache", torch.bfloat16, (sh.num_pages, PAGE, D_QK))
-            if kv_scale is not None:
-                raise ValueError("kv_scale is only used with the fp8 cache")
-        else:
-            _need(kv_cache, "kv_cache", torch.uint8, (sh.num_pages, FP8_PAGE_BYTES))
-            _need(kv_scale, "kv_scale", torch.float32, (sh.num_pages, PAGE))
-        _need(block_table, "block_table", torch.int32, (sh.batch, sh.max_pages_per_seq))
-        _need(src, "src", torch.int32, (sh.batch, self.max_rows))
-        _need(src_lens, "src_lens", torch.int32, (sh.batch,))
+        sh, dev = self.shape, torch.cuda.current_device()
+        _need_cache(dev, sh, kv_cache, kv_scale, block_table)
+        _need_here(dev, src, "src", torch.int32, (sh.batch, self.max_rows))
+        _need_here(dev, src_lens, "src_lens", torch.int32, (sh.batch,))
         if base is not None:
-            _need(base, "base", torch.int32, (sh.batch,))
+            _need_here(dev, base, "base", torch.int32, (sh.batch,))
         if weights is not None:
-            _need(weights, "weights", torch.float32, (sh.batch, sh.max_pages_per_seq * PAGE))
-        _on_current_device(self.workspace, kv_cache, kv_scale, block_table, src, src_lens, base, weights)
+            _need_here(dev, weights, "weights", torch.float32, (sh.batch, sh.max_pages_per_seq * PAGE))
+        _need_here(dev, self.workspace, "the object's workspace", torch.uint8)
         rc = lib().mla_cache_compact(ctypes.byref(sh), _ptr(kv_cache), _ptr(kv_scale), _ptr(block_table), _ptr(src),
                                      _ptr(src_lens), _ptr(base), self.max_rows, _ptr(weights), _ptr(self.workspace),
-                                     self.workspace.numel(), _stream(stream))
+                                     self.workspace.numel(), _stream_of(dev, stream))
         _check(rc, "mla_cache_compact")
 
     def status(self, stream=None) -> int:

@@ -109,7 +109,8 @@ def test_compact_argument_checks():
     assert L.mla_compact_get_device_status(None, None, None) == -1
 
 
-def test_binding_refuses_what_the_kernels_do_not_take():
+def test_binding_refuses_what_the_kernels_do_not_take(monkeypatch):
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
     t = torch.zeros((2, 8), dtype=torch.int32)
     with pytest.raises(ValueError):
         mla.mla_tree_mask(t, torch.zeros((2, 8, 1), dtype=torch.int64))         # CPU tensors
@@ -120,16 +121,23 @@ def test_binding_refuses_what_the_kernels_do_not_take():
 
 
 def test_binding_refuses_tensors_of_another_device(monkeypatch):
-    class On:
-        def __init__(self, index):
-            self.index = index
+    class On(torch.Tensor):
+        """A tensor that says it is on a GPU."""
+        index = 0
 
         def get_device(self):
             return self.index
-    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
-    mla._on_current_device(On(0), None, On(0))
-    with pytest.raises(ValueError):
-        mla._on_current_device(On(0), On(1))
+
+        @property
+        def is_cuda(self):
+            return True
+    t = torch.zeros((2, 3)).as_subclass(On)
+    mla._need_here(0, t, "t", torch.float32, (2, 3))
+    with pytest.raises(ValueError, match="current device"):
+        mla._need_here(1, t, "t", torch.float32, (2, 3))
+    for dtype, shape, error in ((torch.int32, (2, 3), TypeError), (torch.float32, (3, 2), ValueError)):
+        with pytest.raises(error):
+            mla._need_here(0, t, "t", dtype, shape)
 
 
 # ---- the oracle's own pins ----------------------------------------------------
