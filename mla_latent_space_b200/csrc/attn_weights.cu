@@ -59,7 +59,7 @@ constexpr int kHalf = kUnit / 2;
 constexpr uint32_t kWBox = 8192;                 // 64 tokens x 128 bytes
 constexpr uint32_t kWStage = 2 * kWBox;
 constexpr int kWMaxStages = 12;
-constexpr uint32_t kWHead = 3072;                // barriers and column constants
+constexpr uint32_t kWHead = 3 * 1024;            // barriers and column constants
 constexpr uint32_t kWSmem = 232448;
 constexpr int kMaxGroups = 16;                   // groups of row tiles per unit
 constexpr int kSplitBelow = 4;                   // units a pair below which the tiles are grouped
