@@ -42,7 +42,7 @@ cudaError_t launch_tree_mask(const int32_t* parents, const int32_t* draft_lens, 
 size_t attn_weights_workspace_bytes(const mla_shape_t* shape, int num_sms);
 int launch_attn_weights(const mla_shape_t* shape, const void* q, const void* kv, const float* kv_scale,
                         const int32_t* block_table, const int32_t* seqlens, const float* lse, float scale, float decay,
-                        float* weights, void* ws, int num_sms, cudaStream_t stream);
+                        float* weights, void* ws, int num_sms, cudaStream_t stream, int test_stall = 0);
 cudaError_t launch_evict_select(const float* weights, int max_tokens, const int32_t* seqlens, int batch, int budget,
                                 int sink, int recent, int32_t* kept, int32_t* kept_lens, int32_t* status,
                                 cudaStream_t stream);
@@ -260,6 +260,26 @@ int read_status_word(void* workspace, void* stream, int* status) {
   if (cudaStreamSynchronize(st) != cudaSuccess) return MLA_ERR_CUDA;
   *status = (word & kStatusTimeout) ? MLA_ERR_TIMEOUT : word ? MLA_ERR_DEVICE_CHECK : MLA_OK;
   return MLA_OK;
+}
+
+// The checks of mla_attn_weights_fwd, then its launches.
+int attn_weights(const mla_shape_t* shape, const void* q, const void* kv_cache, const float* kv_scale,
+                 const int32_t* block_table, const int32_t* seqlens, const float* lse, float softmax_scale, float decay,
+                 float* weights, void* workspace, size_t workspace_bytes, void* stream, int test_stall) {
+  int rc = check_shape(shape);
+  if (rc != MLA_OK) return rc;
+  if (!q || !kv_cache || !block_table || !seqlens || !lse || !weights || !workspace) return MLA_ERR_INVALID_ARG;
+  if (shape->cache_dtype == MLA_CACHE_FP8_E4M3 && !kv_scale) return MLA_ERR_INVALID_ARG;
+  if (!aligned(q, 16) || !aligned(kv_cache, 256) || !aligned(kv_scale, 4) || !aligned(block_table, 4) ||
+      !aligned(seqlens, 4) || !aligned(lse, 4) || !aligned(weights, 4) || !aligned(workspace, 256))
+    return MLA_ERR_INVALID_ARG;
+  if (!std::isfinite(softmax_scale) || !std::isfinite(decay)) return MLA_ERR_INVALID_ARG;
+  if (shape->batch > 65535 || shape->s_q > 65534) return MLA_ERR_UNSUPPORTED;
+  int sms = 0;
+  if ((rc = device_sms(&sms)) != MLA_OK) return rc;
+  if (workspace_bytes < mla_attn_weights_workspace_bytes(shape, sms)) return MLA_ERR_WORKSPACE;
+  return launch_attn_weights(shape, q, kv_cache, kv_scale, block_table, seqlens, lse, softmax_scale, decay, weights,
+                             workspace, sms, static_cast<cudaStream_t>(stream), test_stall);
 }
 
 }  // namespace
@@ -578,21 +598,20 @@ int mla_attn_weights_fwd(const mla_shape_t* shape, const void* q, const void* kv
                          const int32_t* block_table, const int32_t* seqlens, const float* lse, float softmax_scale,
                          float decay, float* weights, void* workspace, size_t workspace_bytes, void* stream) {
   CallRange range_("mla_attn_weights_fwd");
-  int rc = check_shape(shape);
-  if (rc != MLA_OK) return rc;
-  if (!q || !kv_cache || !block_table || !seqlens || !lse || !weights || !workspace) return MLA_ERR_INVALID_ARG;
-  if (shape->cache_dtype == MLA_CACHE_FP8_E4M3 && !kv_scale) return MLA_ERR_INVALID_ARG;
-  if (!aligned(q, 16) || !aligned(kv_cache, 256) || !aligned(kv_scale, 4) || !aligned(block_table, 4) ||
-      !aligned(seqlens, 4) || !aligned(lse, 4) || !aligned(weights, 4) || !aligned(workspace, 256))
-    return MLA_ERR_INVALID_ARG;
-  if (!std::isfinite(softmax_scale) || !std::isfinite(decay)) return MLA_ERR_INVALID_ARG;
-  if (shape->batch > 65535 || shape->s_q > 65534) return MLA_ERR_UNSUPPORTED;
-  int sms = 0;
-  if ((rc = device_sms(&sms)) != MLA_OK) return rc;
-  if (workspace_bytes < mla_attn_weights_workspace_bytes(shape, sms)) return MLA_ERR_WORKSPACE;
-  return launch_attn_weights(shape, q, kv_cache, kv_scale, block_table, seqlens, lse, softmax_scale, decay, weights,
-                             workspace, sms, static_cast<cudaStream_t>(stream));
+  return attn_weights(shape, q, kv_cache, kv_scale, block_table, seqlens, lse, softmax_scale, decay, weights, workspace,
+                      workspace_bytes, stream, 0);
 }
+
+#ifdef MLA_TEST_ENTRY_POINTS
+// Test-only entry point: mla_attn_weights_fwd with the kernel's stall hook set.
+int mla_test_attn_weights_stalled(const mla_shape_t* shape, const void* q, const void* kv_cache, const float* kv_scale,
+                                  const int32_t* block_table, const int32_t* seqlens, const float* lse,
+                                  float softmax_scale, float decay, float* weights, void* workspace,
+                                  size_t workspace_bytes, void* stream) {
+  return attn_weights(shape, q, kv_cache, kv_scale, block_table, seqlens, lse, softmax_scale, decay, weights, workspace,
+                      workspace_bytes, stream, 1);
+}
+#endif
 
 int mla_attn_weights_get_device_status(void* workspace, void* stream, int* status) {
   return read_status_word(workspace, stream, status);

@@ -88,6 +88,7 @@ constexpr double kTruncation = 4e-7;
 
 struct WBars {
   uint64_t full[kWMaxStages], empty[kWMaxStages], q_full[9], q_free[9], d_full[2], d_empty[2], part_full[2], done;
+  uint64_t never;   // test hook: nothing arrives on it (WArgs::test_stall)
   uint32_t tmem_base;
   int32_t abort;
   int32_t r0, base0;
@@ -113,6 +114,7 @@ struct WArgs {
   float* partial;            // [groups][units][256]
   float sl2, decay;
   int batch, s_q, heads, rows, causal, max_pages, num_pages, max_units;
+  int test_stall;            // 0 in every product call
 };
 
 // What every role derives from the lengths.
@@ -283,6 +285,7 @@ attn_weights_kernel(const __grid_constant__ CUtensorMap pool_map, const __grid_c
       mbar_init(bar(bars->part_full[s]), 4);    // the second warpgroup's warps
     }
     mbar_init(bar(bars->done), 1);
+    mbar_init(bar(bars->never), 1);
     bars->abort = 0;
     fence_mbar_init();
     tma_prefetch_desc(&pool_map);
@@ -444,6 +447,7 @@ attn_weights_kernel(const __grid_constant__ CUtensorMap pool_map, const __grid_c
       const uint64_t ad0 = w_desc(ring), bd0 = w_desc(q_base);
       const uint32_t qs = q_stride >> 4;
       each_seg(a, plan, [&](const Seg& sg) {
+        if (a.test_stall && !w_warp_wait(ctl, bar(bars->never), 0)) return false;
         const uint32_t ib = idesc_bf16(2 * sg.nh), i8 = idesc_e4m3(2 * sg.nh);
         for (int u = sg.u0; u < sg.u1; ++u, ++units) {
           const uint32_t buf = units & 1u, d = tmem + 256u * buf;
@@ -740,7 +744,7 @@ size_t attn_weights_workspace_bytes(const mla_shape_t* shape, int num_sms) { ret
 
 int launch_attn_weights(const mla_shape_t* shape, const void* q, const void* kv, const float* kv_scale,
                         const int32_t* block_table, const int32_t* seqlens, const float* lse, float scale, float decay,
-                        float* weights, void* ws, int num_sms, cudaStream_t stream) {
+                        float* weights, void* ws, int num_sms, cudaStream_t stream, int test_stall) {
   const bool fp8 = shape->cache_dtype == MLA_CACHE_FP8_E4M3;
   const WLayout L = w_layout(shape, num_sms);
   char* w = static_cast<char*>(ws);
@@ -761,7 +765,8 @@ int launch_attn_weights(const mla_shape_t* shape, const void* q, const void* kv,
           reinterpret_cast<const float*>(w + L.q_scale), weights, w, reinterpret_cast<uint32_t*>(w + L.counters),
           reinterpret_cast<float*>(w + L.partial),
           float(double(scale) * 1.4426950408889634 * (fp8 ? 1.0 : 1.0 + kTruncation)), decay, shape->batch, shape->s_q,
-          shape->num_heads, rows, shape->causal, shape->max_pages_per_seq, shape->num_pages, L.max_units};
+          shape->num_heads, rows, shape->causal, shape->max_pages_per_seq, shape->num_pages, L.max_units,
+          test_stall};
   if (fp8) {
     split_query_kernel<<<(q_rows + 7) / 8, 256, 0, stream>>>(static_cast<const uint16_t*>(q), q_rows,
                                                               reinterpret_cast<uint8_t*>(w + L.q8),

@@ -30,6 +30,15 @@ int mla_test_decode_stalled(const mla_shape_t* shape, const void* q, const void*
                             void* workspace, size_t workspace_bytes, void* out, float* lse,
                             void* stream);
 
+/* mla_attn_weights_fwd with its kernel's test hook set: the MMA issuers wait
+ * on a barrier that nothing arrives on, which runs out after about 2 s and
+ * runs the abort path.  mla_attn_weights_get_device_status then reports
+ * MLA_ERR_TIMEOUT; the weights are not valid.  Faults nothing. */
+int mla_test_attn_weights_stalled(const mla_shape_t* shape, const void* q, const void* kv_cache, const float* kv_scale,
+                                  const int32_t* block_table, const int32_t* seqlens, const float* lse,
+                                  float softmax_scale, float decay, float* weights, void* workspace,
+                                  size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -218,6 +218,35 @@ def test_infinite_lse_and_empty_batches():
     assert st == 0 and np.array_equal(got, old)
 
 
+@pytest.mark.parametrize("cache", ["bf16", "fp8"])
+def test_a_wait_that_runs_out_is_reported_and_the_context_stays_usable(cache):
+    """The test library's stalled call makes the MMA issuers wait for what
+    never comes: after 2 s the kernel reports it, drains and returns."""
+    import ctypes
+    import time
+    from gpu_helpers import test_lib
+    fn = test_lib().mla_test_attn_weights_stalled
+    fn.argtypes, fn.restype = mla.lib().mla_attn_weights_fwd.argtypes, ctypes.c_int
+    wl = mw.make(2, 2, 128, [3000, 100], seed=94, cache_dtype=cache)
+    lse, old = lse_of(wl), old_weights(wl)
+    dev, acc = to_device(wl), mla.AttnWeights(shape_of(wl))
+    l_dev, w = torch.from_numpy(lse).cuda(), torch.from_numpy(old).cuda()
+    ptr = lambda t: None if t is None else t.data_ptr()
+    torch.cuda.synchronize()
+    t0 = time.perf_counter()
+    rc = fn(ctypes.byref(acc.shape), ptr(dev["q"]), ptr(dev["pool"]), ptr(dev["kv_scale"]), ptr(dev["block_table"]),
+            ptr(dev["seqlens"]), ptr(l_dev), wl.softmax_scale, 0.5, ptr(w), ptr(acc.workspace), acc.workspace.numel(),
+            torch.cuda.current_stream().cuda_stream)
+    assert rc == 0
+    torch.cuda.synchronize()
+    assert 1.0 < time.perf_counter() - t0 < 30.0
+    assert acc.status() == -5 and acc.status() == 0
+    acc.workspace.zero_()                                               # as the header asks after a timeout
+    got, st = run(wl, lse, 0.5, old, acc, dev)
+    assert st == 0
+    assert_close(wl, got, lse, 0.5, old)
+
+
 def test_binding_checks():
     wl = mw.make(2, 1, 16, [100, 70], seed=91)
     dev, acc = to_device(wl), mla.AttnWeights(shape_of(wl))
