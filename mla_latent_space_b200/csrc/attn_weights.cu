@@ -25,11 +25,13 @@
 //
 // Split.  The work is (request, 256-token unit, tile of rows).  Every pair
 // counts the units from the lengths and takes an equal share, in the order
-// (request, group of tiles, unit).  With enough units to fill the machine
-// the tiles form one group and a unit's weights stay with one thread; with
-// fewer than 4 a pair, the tiles are cut into up to 16 groups whose sums go
-// through the workspace, and the last group to finish a unit adds them in
-// their order: no order of sums depends on timing.
+// (request, group of tiles, unit).  The tiles form one group, and a unit's
+// weights stay with one thread, unless there are fewer than 4 units a pair
+// and more groups shorten the longest pair's work (16 queries x 128 heads,
+// b=16, t=4096: 122 us in two groups, 130 in one; 4 queries, b=1, t=32768: 30
+// in one, 36 in two).  The groups' sums then go through the workspace, and the
+// last group to finish a unit adds them in their order: no order of sums
+// depends on timing.
 //
 // FP8 cache: the e4m3 bytes go to the tensor core as they are (kind::f8f6f4)
 // against a two-part e4m3 copy of the query (hi + lo with a power-of-two
@@ -62,7 +64,7 @@ constexpr int kWMaxStages = 12;
 constexpr uint32_t kWHead = 3 * 1024;            // barriers and column constants
 constexpr uint32_t kWSmem = 232448;
 constexpr int kMaxGroups = 16;                   // groups of row tiles per unit
-constexpr int kSplitBelow = 4;                   // units a pair below which the tiles are grouped
+constexpr int kSplitBelow = 4;                   // units a pair below which the tiles may be grouped
 constexpr uint64_t kWTimeoutNs = 2000000000ull;
 constexpr uint32_t kEpiBar = 1;
 
@@ -330,15 +332,22 @@ attn_weights_kernel(const __grid_constant__ CUtensorMap pool_map, const __grid_c
       before += k < warp ? warp_sum[k] : 0;
       total += warp_sum[k];
     }
-    // tiles of rows: as many rows as a tile holds, but 128 where that leaves
-    // pairs without work
-    int tile = min(W<kFp8>::tile, (a.rows + 63) / 64 * 64);
-    if (tile > 128 && int64_t(total) * ((a.rows + tile - 1) / tile) < pairs) tile = 128;
-    plan.tile = tile;
-    plan.tiles = (a.rows + tile - 1) / tile;
-    plan.groups = total >= kSplitBelow * pairs || total == 0
-                      ? 1
-                      : min(min(plan.tiles, kMaxGroups), (kSplitBelow * pairs + total - 1) / total);
+    plan.tile = min(W<kFp8>::tile, (a.rows + 63) / 64 * 64);
+    plan.tiles = (a.rows + plan.tile - 1) / plan.tile;
+    // groups of tiles: as many as make the longest pair's steps (a unit
+    // against a tile) fewest; an item of more than one group costs half a
+    // step more for the workspace
+    plan.groups = 1;
+    if (total < kSplitBelow * pairs) {
+      int64_t fewest = int64_t((total + pairs - 1) / pairs) * (2 * plan.tiles);   // half steps
+      for (int g = 2; g <= min(plan.tiles, kMaxGroups); ++g) {
+        const int64_t steps = int64_t((total * g + pairs - 1) / pairs) * (2 * ((plan.tiles + g - 1) / g) + 1);
+        if (steps < fewest) {
+          fewest = steps;
+          plan.groups = g;
+        }
+      }
+    }
     const int64_t cost = int64_t(total) * plan.tiles;
     plan.c0 = cost * pair / pairs;
     plan.c1 = cost * (pair + 1) / pairs;

@@ -13,10 +13,12 @@
 // key > thr and the first `need` of those with key == thr.
 //
 // Layout.  The weights are read once: the keys stay in shared memory.  A row
-// of up to kWideTokens tokens is one CTA's work; a longer one is cut into
-// contiguous chunks over a cluster of 8 CTAs, which add up each other's
-// histograms and counts over distributed shared memory.  Rows too long even
-// for that re-read the weights through L2 in every pass.  What bounds it is
+// is one CTA's work, or it is cut into contiguous chunks over a cluster of 8
+// CTAs, which add up each other's histograms and counts over distributed
+// shared memory.  Rows too long even for that re-read the weights through L2
+// in every pass.  The cluster pays for long rows in small batches (us, one
+// CTA / cluster; batches of 4, 32, 64: 8192 tokens 13 / 14, - , 13 / 27;
+// 32768 tokens 25 / 15, 25 / 18, 25 / 32; 49152 tokens at 32: 33 / 20).  What bounds it is
 // latency: of the 16 us of two rows of 131072 tokens, 3.5 are the trip to
 // memory, 5 the digits' passes with their cluster barriers, 5 the ordered
 // output.  (Adding up equal bins within a warp before the shared-memory adds,
@@ -38,7 +40,8 @@ constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kBins = 2048;
 constexpr int kPasses = 3;
 constexpr int kCluster = 8;
-constexpr int kWideTokens = 8192;
+constexpr int kWideTokens = 8192;            // up to here, or in batches above kWideBatch, one CTA a row
+constexpr int kWideBatch = 32;
 constexpr int kSmemKeys = 48 * 1024;         // keys per CTA that fit beside the histograms (192 KB)
 
 struct alignas(16) SelShared {
@@ -249,7 +252,7 @@ cudaError_t launch(const float* weights, int max_tokens, const int32_t* seqlens,
   auto fn = &evict_select_kernel<kCtas, kInSmem>;
   const int chunk = ((max_tokens + kCtas - 1) / kCtas + 31) & ~31;
   const size_t smem = kInSmem ? size_t(chunk) * 4 : 0;
-  if (!ensure_smem_attr(reinterpret_cast<const void*>(fn), kInSmem ? (kCtas > 1 ? kSmemKeys : kWideTokens) * 4 : 0))
+  if (!ensure_smem_attr(reinterpret_cast<const void*>(fn), kInSmem ? kSmemKeys * 4 : 0))
     return cudaErrorInvalidValue;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(unsigned(batch) * kCtas);
@@ -273,7 +276,8 @@ cudaError_t launch(const float* weights, int max_tokens, const int32_t* seqlens,
 cudaError_t launch_evict_select(const float* weights, int max_tokens, const int32_t* seqlens, int batch, int budget,
                                 int sink, int recent, int32_t* kept, int32_t* kept_lens, int32_t* status,
                                 cudaStream_t stream) {
-  const auto fn = max_tokens <= kWideTokens              ? &launch<1, true>
+  const bool one = max_tokens <= kWideTokens || (batch > kWideBatch && max_tokens <= kSmemKeys);
+  const auto fn = one                                   ? &launch<1, true>
                   : max_tokens <= kCluster * kSmemKeys ? &launch<kCluster, true>
                                                          : &launch<kCluster, false>;
   return fn(weights, max_tokens, seqlens, batch, budget, sink, recent, kept, kept_lens, status, stream);

@@ -77,6 +77,13 @@ def test_select_wide_batch_and_short_requests():
     check_select(w, [(r * 7) % (T + 1) for r in range(b)], 20, 2, 5)
 
 
+def test_select_large_batch_of_long_rows():
+    b, T = 40, 49152                            # one CTA holds a whole long row
+    w = weights(b, T, 6)
+    w[::3] = weights(len(w[::3]), T, 7, "ties")
+    check_select(w, [T - 3 * r for r in range(b)], 4000, 4, 100)
+
+
 def test_select_budget_larger_than_the_row():
     check_select(weights(2, 64, 4), [64, 0], 200, 4, 8)
 
