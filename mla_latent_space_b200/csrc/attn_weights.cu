@@ -27,11 +27,11 @@
 // counts the units from the lengths and takes an equal share, in the order
 // (request, group of tiles, unit).  The tiles form one group, and a unit's
 // weights stay with one thread, unless there are fewer than 4 units a pair
-// and more groups shorten the longest pair's work (16 queries x 128 heads,
-// b=16, t=4096: 122 us in two groups, 130 in one; 4 queries, b=1, t=32768: 30
-// in one, 36 in two).  The groups' sums then go through the workspace, and the
-// last group to finish a unit adds them in their order: no order of sums
-// depends on timing.
+// and more groups shorten the longest pair's work (us in 1, 2, 4, 8 groups,
+// 128 heads: 16 queries of 16 x 4096 tokens 129, 123, 128, 132; of 1 x 4096
+// 44, 33, 26, 28; 5 queries of 6 x 6000 36, 41, 38, 37).  The groups' sums
+// then go through the workspace, and the last group to finish a unit adds
+// them in their order: no order of sums depends on timing.
 //
 // FP8 cache: the e4m3 bytes go to the tensor core as they are (kind::f8f6f4)
 // against a two-part e4m3 copy of the query (hi + lo with a power-of-two
@@ -334,16 +334,20 @@ attn_weights_kernel(const __grid_constant__ CUtensorMap pool_map, const __grid_c
     }
     plan.tile = min(W<kFp8>::tile, (a.rows + 63) / 64 * 64);
     plan.tiles = (a.rows + plan.tile - 1) / plan.tile;
-    // groups of tiles: as many as make the longest pair's steps (a unit
-    // against a tile) fewest; an item of more than one group costs half a
-    // step more for the workspace
+    // groups of tiles: the number that makes the longest pair's time least, in
+    // tenths of a step (a unit against a tile).  A pair takes `items` units of
+    // a group of `len` tiles, or its even share and one item; each tile of a
+    // run costs 0.6 steps to load its rows, each item of more than one group
+    // 0.6 for the workspace.
     plan.groups = 1;
     if (total < kSplitBelow * pairs) {
-      int64_t fewest = int64_t((total + pairs - 1) / pairs) * (2 * plan.tiles);   // half steps
-      for (int g = 2; g <= min(plan.tiles, kMaxGroups); ++g) {
-        const int64_t steps = int64_t((total * g + pairs - 1) / pairs) * (2 * ((plan.tiles + g - 1) / g) + 1);
-        if (steps < fewest) {
-          fewest = steps;
+      const int64_t share = (int64_t(total) * plan.tiles + pairs - 1) / pairs;
+      int64_t least = 0;
+      for (int g = 1; g <= min(plan.tiles, kMaxGroups); g *= 2) {
+        const int64_t len = (plan.tiles + g - 1) / g, items = (int64_t(total) * g + pairs - 1) / pairs;
+        const int64_t time = 10 * min(items * len, share + len) + 6 * len + (g > 1 ? 6 * items : 0);
+        if (g == 1 || time < least) {
+          least = time;
           plan.groups = g;
         }
       }

@@ -96,9 +96,10 @@ def test_weights_over_many_units_and_repeated_calls_agree_bit_for_bit():
 
 
 @pytest.mark.parametrize("cache", ["bf16", "fp8"])
-def test_weights_when_groups_of_tiles_meet_in_the_workspace(cache):
-    # few units and many rows: each unit's tiles are shared between pairs, in groups of unequal size
-    wl = mw.make(3, 5, 120, [9000, 14000, 700], causal=True, seed=92, cache_dtype=cache)
+@pytest.mark.parametrize("s,heads,lens", [(5, 120, [9000, 14000, 700]), (16, 128, [12000]), (11, 100, [3000, 9, 5000])])
+def test_weights_when_groups_of_tiles_meet_in_the_workspace(cache, s, heads, lens):
+    # few units and many rows: each unit's tiles are shared between pairs, in groups of several and of unequal size
+    wl = mw.make(len(lens), s, heads, lens, causal=True, seed=92, cache_dtype=cache)
     lse, old = lse_of(wl), old_weights(wl)
     acc, dev = mla.AttnWeights(shape_of(wl)), to_device(wl)
     a, st = run(wl, lse, 0.75, old, acc, dev)
