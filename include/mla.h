@@ -297,7 +297,9 @@ int mla_tree_decode_fwd(const mla_shape_t* shape, const void* q, const void* kv_
                         const int32_t* block_table, const int32_t* seqlens, const int32_t* draft_lens,
                         const int64_t* tree_mask, float softmax_scale, void* workspace, size_t workspace_bytes,
                         void* out, float* lse, void* stream);
-/* Device status of the tree decode's kernels; as mla_get_device_status. */
+/* Reads and clears the device status of the tree decode's kernels, the
+ * scheduler's among them: what any call since the last read flagged.
+ * SYNCHRONISES `stream`. */
 int mla_tree_get_device_status(const mla_shape_t* shape, int num_sms, void* workspace, void* stream, int* status);
 
 /* Mask rows of trees given by their parents: bit d of row i is set when node

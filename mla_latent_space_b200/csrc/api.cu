@@ -258,7 +258,10 @@ int read_status_word(void* workspace, void* stream, int* status) {
   if (cudaStreamSynchronize(st) != cudaSuccess) return MLA_ERR_CUDA;
   if (cudaMemsetAsync(workspace, 0, 4, st) != cudaSuccess) return MLA_ERR_CUDA;
   if (cudaStreamSynchronize(st) != cudaSuccess) return MLA_ERR_CUDA;
-  *status = (word & kStatusTimeout) ? MLA_ERR_TIMEOUT : word ? MLA_ERR_DEVICE_CHECK : MLA_OK;
+  *status = (word & kStatusTimeout)     ? MLA_ERR_TIMEOUT
+            : (word & kStatusWorkspace) ? MLA_ERR_WORKSPACE
+            : word                      ? MLA_ERR_DEVICE_CHECK
+                                        : MLA_OK;
   return MLA_OK;
 }
 
@@ -571,6 +574,7 @@ int mla_tree_decode_fwd(const mla_shape_t* shape, const void* q, const void* kv_
   si.tree = 1;
   si.draft_lens = draft_lens;
   si.overhead = tree_overhead(shape);
+  si.sticky = static_cast<int32_t*>(ws);
   if (launch_schedule(seqlens, si, num_workers_for(sms), static_cast<int32_t*>(sched), st) != cudaSuccess)
     return MLA_ERR_CUDA;
   const TreeArgs tree{draft_lens, tree_mask, (shape->s_q + 63) / 64};
@@ -585,8 +589,7 @@ int mla_tree_decode_fwd(const mla_shape_t* shape, const void* q, const void* kv_
 int mla_tree_get_device_status(const mla_shape_t* shape, int num_sms, void* workspace, void* stream, int* status) {
   TreeLayout L;
   if (!workspace || !status || !tree_layout(shape, num_sms, &L)) return MLA_ERR_INVALID_ARG;
-  char* w = static_cast<char*>(workspace);
-  return mla_get_device_status(w + L.sched, w + L.ws, stream, status);
+  return read_status_word(static_cast<char*>(workspace) + L.ws, stream, status);
 }
 
 size_t mla_attn_weights_workspace_bytes(const mla_shape_t* shape, int num_sms) {

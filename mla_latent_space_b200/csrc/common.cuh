@@ -69,6 +69,9 @@ struct ShapeInfo {
   int tree = 0;
   const int32_t* draft_lens = nullptr;
   int overhead = kPieceOverhead;   // of a piece, in pages (tree decode: kTreeOverhead*)
+  // tree decode: a device word that keeps what a schedule flags until it is
+  // read (the schedule, and its own status, is rebuilt by every call)
+  int32_t* sticky = nullptr;
 };
 
 // Nodes of request r's drafted tree: the last n of its t tokens.  A count

@@ -178,6 +178,7 @@ schedule_kernel(const int32_t* __restrict__ seqlens, ShapeInfo s, int W, int32_t
   if (flag) atomicOr(&flag_sh, flag);
   int64_t excl;
   const int64_t total = block_exclusive_scan(local, warp_tot, &excl);
+  if (tid == 0 && s.sticky != nullptr && flag_sh != 0) atomicOr(s.sticky, flag_sh);
   for (int T = t0; T < t1; ++T) {
     prefix_sm[T] = int32_t(excl);
     tiles[size_t(T) * kTileInts + T_PAGES] = pages_sm[T];
@@ -374,7 +375,10 @@ namespace {
 // tens of thousands of tiles).
 __global__ void schedule_kernel_global(const int32_t* seqlens, ShapeInfo s, int W, int32_t* sched) {
   ptx::griddep_launch_dependents();   // as in schedule_kernel
-  if (threadIdx.x == 0 && blockIdx.x == 0) plan_schedule_seq(seqlens, s, W, sched);
+  if (threadIdx.x == 0 && blockIdx.x == 0) {
+    plan_schedule_seq(seqlens, s, W, sched);
+    if (s.sticky != nullptr && sched[H_STATUS] != 0) atomicOr(s.sticky, sched[H_STATUS]);
+  }
 }
 }  // namespace
 

@@ -235,3 +235,30 @@ def test_binding_checks():
         dec.decode(*args, mask, 0.1, out, lse, draft_lens=torch.zeros(3, dtype=torch.int32, device="cuda"))
     with pytest.raises(mla.MLAError):
         mla.TreeDecoder(mla.make_shape(2, 4, 16, 2, 4, causal=True))
+
+
+@pytest.mark.parametrize("what", ["count", "length"])
+def test_status_stays_until_it_is_read_and_is_cleared_by_the_read(what):
+    # several steps are enqueued before the host looks: a flag of one of them outlives the good steps behind it
+    wl = mw.make(2, 4, 16, [100, 30], seed=110)
+    dev, dec = to_device(wl), mla.TreeDecoder(shape_of(wl))
+    mask = torch.from_numpy(oracle.tree_mask(parents_of(2, 4, seed=111))).cuda()
+    out = torch.empty((2, 4, 16, 512), dtype=torch.bfloat16, device="cuda")
+    lse = torch.empty((2, 4, 16), dtype=torch.float32, device="cuda")
+    good = torch.tensor([4, 2], dtype=torch.int32, device="cuda")
+    bad_count = torch.tensor([5, 2], dtype=torch.int32, device="cuda")
+    bad_length = torch.tensor([wl.max_pages * 64 + 1, 30], dtype=torch.int32, device="cuda")
+
+    def step(lens, seqlens):
+        dec.decode(dev["q"], dev["pool"], dev["block_table"], seqlens, mask, wl.softmax_scale, out, lse, draft_lens=lens)
+    step(good, dev["seqlens"])
+    assert dec.status() == 0
+    if what == "count":
+        step(bad_count, dev["seqlens"])
+    else:
+        step(good, bad_length)
+    step(good, dev["seqlens"])
+    assert dec.status() == -6
+    assert dec.status() == 0
+    step(good, dev["seqlens"])
+    assert dec.status() == 0
