@@ -77,16 +77,14 @@ struct W {
 };
 
 // BF16: the tensor core's fp32 accumulator drops what does not fit, always
-// towards zero.  Given a score x, the expected partial sum after k of the 36
-// steps is x k / 36 (columns in any order), a step loses a quarter of its
-// last place on average (the accumulator behaves as if it kept one bit more
-// than it returns), a last place is on average 0.72 * 2^-23 of the value, so
-// x comes out smaller by 18 * 0.25 * 0.72 * 2^-23 = 3.9e-7 of itself.  The
-// scale makes up for that: the weights' mean error goes from -1.4e-6 to
-// -1.7e-7 of themselves, their relative error from 1.9e-6 to 4.6e-7 (b=4,
-// h=128, up to 4096 tokens).  FP8's two shorter sums lose too little to
-// matter (-3e-7).
-constexpr double kTruncation = 4e-7;
+// towards zero, and the scores of random values come out smaller by about
+// 4e-7 of themselves.  The scale does not make up for that: the lse that
+// belongs to a call is the decode's, whose scores went through the same 36
+// steps, so in x - lse most of it is gone.  Mean (rms) error of a weight
+// against attention in 64 bits, h=128, t=4096: 2.8e-7 (5.4e-7) with the
+// decode's lse, -1.3e-6 (1.4e-6) with an exact one.  (A scale larger by 4e-7
+// gave 1.5e-6 (1.5e-6) and -1.5e-7 (3.1e-7), and put scores whose sums are
+// exact off by 4e-7 of the score.)  FP8's two shorter sums lose less.
 
 struct WBars {
   uint64_t full[kWMaxStages], empty[kWMaxStages], q_full[9], q_free[9], d_full[2], d_empty[2], part_full[2], done;
@@ -777,9 +775,8 @@ int launch_attn_weights(const mla_shape_t* shape, const void* q, const void* kv,
   WArgs a{static_cast<const uint8_t*>(kv), kv_scale, block_table, seqlens, lse,
           reinterpret_cast<const float*>(w + L.q_scale), weights, w, reinterpret_cast<uint32_t*>(w + L.counters),
           reinterpret_cast<float*>(w + L.partial),
-          float(double(scale) * 1.4426950408889634 * (fp8 ? 1.0 : 1.0 + kTruncation)), decay, shape->batch, shape->s_q,
-          shape->num_heads, rows, shape->causal, shape->max_pages_per_seq, shape->num_pages, L.max_units,
-          test_stall};
+          float(double(scale) * 1.4426950408889634), decay, shape->batch, shape->s_q, shape->num_heads, rows,
+          shape->causal, shape->max_pages_per_seq, shape->num_pages, L.max_units, test_stall};
   if (fp8) {
     split_query_kernel<<<(q_rows + 7) / 8, 256, 0, stream>>>(static_cast<const uint16_t*>(q), q_rows,
                                                               reinterpret_cast<uint8_t*>(w + L.q8),

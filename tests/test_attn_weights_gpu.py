@@ -260,3 +260,25 @@ def test_binding_checks():
         acc.accumulate(*args, lse.double(), 0.1, 0.5, w)
     with pytest.raises(mla.MLAError):
         acc.accumulate(*args, lse, 0.1, float("nan"), w)
+
+
+def test_scores_that_are_exact_give_weights_as_near_as_their_exponent():
+    """Whole numbers whose products and sums the accumulator holds exactly: x = 576 - k, lse = 576, a weight of e^-k.
+
+    The exponent x log2(e) - lse log2(e) is one fused multiply-add of the rounded scale and the rounded lse: off by
+    at most 2^-24 (|x| + |lse|) log2(e) and half a step of the result, and a weight by ln 2 times that (1152 * 2^-24 =
+    6.9e-5); exp2 and the sum of four equal terms by 2^-20 more.
+    """
+    wl = mw.make(1, 1, 4, [200], seed=112)
+    wl.softmax_scale = 1.0
+    wl.q[:] = 1.0
+    k = np.arange(200) % 60
+    rows = torch.ones((200, 576), dtype=torch.bfloat16)
+    for j in range(200):
+        rows[j, 7 * j % 500:7 * j % 500 + k[j]] = 0.0
+    for j in range(200):
+        wl.pool[wl.block_table[0, j // 64], j % 64] = rows[j]
+    got, st = run(wl, np.full((1, 1, 4), 576.0, dtype=np.float32), 0.0, old_weights(wl))
+    ref = 4.0 * np.exp(-k.astype(np.float64))
+    assert st == 0
+    assert (np.abs(got[0, :200] - ref) <= (1152 * 2.0 ** -24 + 2.0 ** -20) * ref).all()
