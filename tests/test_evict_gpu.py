@@ -296,3 +296,60 @@ def test_binding_checks():
         comp.compact(pool, bt, kept[:, :7], lens)
     with pytest.raises(ValueError):
         comp.compact(pool, bt, kept, lens, kv_scale=torch.zeros((4, 64), device="cuda"))
+
+
+def moved(cache, pool, sc, w, bt, src, lens, base):
+    """The same move by plain indexing on the device (every destination is written once)."""
+    b, rows = src.shape
+    k = torch.arange(rows, device="cuda")
+    r, k = (k < lens[:, None]).nonzero(as_tuple=True)
+    a, d = src[r, k].long(), k + (0 if base is None else base[r].long())
+    at = lambda pos: (bt[r, pos // 64].long(), pos % 64)
+    pool, sc, w = pool.clone(), None if sc is None else sc.clone(), w.clone()
+    if cache == "bf16":
+        pool[at(d)] = pool[at(a)]
+    else:
+        for plane in (pool[:, :32768].unflatten(1, (64, 512)), pool[:, 32768:].unflatten(1, (64, 128))):
+            plane[at(d)] = plane[at(a)]
+        sc[at(d)] = sc[at(a)]
+    w[r, d] = w[r, a]
+    return pool, sc, w
+
+
+@pytest.mark.parametrize("cache", ["bf16", "fp8"])
+@pytest.mark.parametrize("b,rows,t,kind", [
+    (64, 2048, 2300, "shift"),      # 64 (FP8: 32) groups a request: seven (four) for each resident CTA
+    (64, 4096, 4400, "shift"),
+    (64, 4096, 8192, "random"),
+    (1, 81920, 100000, "shift"),    # one long list: most groups wait
+    (700, 130, 200, "shift"),       # more requests than resident CTAs, several groups each: a CTA's request changes
+    (299, 200, 400, "random"),
+])
+def test_compact_in_many_rounds(cache, b, rows, t, kind):
+    g = torch.Generator(device="cuda").manual_seed(rows + b)
+    pages = (t + 63) // 64
+    bt = torch.randperm(b * pages, generator=g, device="cuda").to(torch.int32).view(b, pages)
+    if cache == "bf16":
+        pool = torch.randint(-2**15, 2**15, (b * pages, 64, 576), generator=g, dtype=torch.int16, device="cuda").view(torch.bfloat16)
+        sc = None
+    else:
+        pool = torch.randint(0, 256, (b * pages, 40960), generator=g, dtype=torch.uint8, device="cuda")
+        sc = torch.rand((b * pages, 64), generator=g, device="cuda")
+    w = torch.rand((b, pages * 64), generator=g, device="cuda")
+    if kind == "shift":             # each row that is overwritten is itself moved
+        shift = torch.tensor([1, 31, 32, 33, 63, 64, 65, t - rows], device="cuda").repeat(b)[:b]
+        src = torch.arange(rows, device="cuda") + shift.clamp(max=t - rows)[:, None]
+    else:
+        src = torch.rand((b, t), generator=g, device="cuda").argsort(1)[:, :rows].sort(1).values
+    src = src.to(torch.int32).contiguous()
+    comp = mla.CacheCompactor(mla.make_shape(b, 1, 1, pages, b * pages, cache), rows)
+    bits = lambda x: x.view(torch.int16) if x.dtype == torch.bfloat16 else x
+    for call in range(3):           # through one workspace
+        lens = torch.full((b,), rows, dtype=torch.int32, device="cuda")
+        if call > 0 and b > 1:
+            lens = torch.randint(0, rows + 1, (b,), generator=g, device="cuda", dtype=torch.int32)
+        p_ref, s_ref, w_ref = moved(cache, pool, sc, w, bt, src, lens, None)
+        comp.compact(pool, bt, src, lens, kv_scale=sc, weights=w)
+        assert comp.status() == 0
+        assert torch.equal(bits(pool), bits(p_ref)) and torch.equal(w, w_ref)
+        assert sc is None or torch.equal(sc, s_ref)
