@@ -386,7 +386,10 @@ int mla_evict_select(int32_t batch, int32_t max_tokens, const float* weights, co
  *             aligned, zero-filled before its first use; calls that may
  *             overlap in time need one each.
  * A page that two requests share (or one request lists twice) must lie where
- * nothing moves: before the first entry with src[r][k] != base + k. */
+ * nothing moves: before the first entry with src[r][k] != base + k.
+ * After MLA_ERR_TIMEOUT some of the listed rows have moved and others have
+ * not: the rows of every request of the call are not valid, and the call must
+ * not be repeated with its lists.  The workspace can be used again. */
 size_t mla_compact_workspace_bytes(const mla_shape_t* shape, int max_rows);
 int mla_cache_compact(const mla_shape_t* shape, void* kv_cache, float* kv_scale, const int32_t* block_table,
                       const int32_t* src, const int32_t* src_lens, const int32_t* base, int32_t max_rows, float* weights,

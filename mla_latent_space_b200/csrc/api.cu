@@ -49,7 +49,7 @@ cudaError_t launch_evict_select(const float* weights, int max_tokens, const int3
 size_t compact_workspace_bytes(const mla_shape_t* shape, int max_rows);
 int launch_compact(const mla_shape_t* shape, void* kv, float* kv_scale, const int32_t* block_table, const int32_t* src,
                    const int32_t* src_lens, const int32_t* base, int max_rows, float* weights, void* ws, int num_sms,
-                   cudaStream_t stream);
+                   cudaStream_t stream, int test_stall = 0);
 }  // namespace mla
 
 using namespace mla;
@@ -283,6 +283,26 @@ int attn_weights(const mla_shape_t* shape, const void* q, const void* kv_cache, 
   if (workspace_bytes < mla_attn_weights_workspace_bytes(shape, sms)) return MLA_ERR_WORKSPACE;
   return launch_attn_weights(shape, q, kv_cache, kv_scale, block_table, seqlens, lse, softmax_scale, decay, weights,
                              workspace, sms, static_cast<cudaStream_t>(stream), test_stall);
+}
+
+// The checks of mla_cache_compact, then its launch.
+int cache_compact(const mla_shape_t* shape, void* kv_cache, float* kv_scale, const int32_t* block_table, const int32_t* src,
+                  const int32_t* src_lens, const int32_t* base, int32_t max_rows, float* weights, void* workspace,
+                  size_t workspace_bytes, void* stream, int test_stall) {
+  int rc = check_shape(shape);
+  if (rc != MLA_OK) return rc;
+  if (!kv_cache || !block_table || !src || !src_lens || !workspace || max_rows < 1) return MLA_ERR_INVALID_ARG;
+  if (shape->cache_dtype == MLA_CACHE_FP8_E4M3 && !kv_scale) return MLA_ERR_INVALID_ARG;
+  if (!aligned(kv_cache, 256) || !aligned(kv_scale, 4) || !aligned(block_table, 4) || !aligned(src, 4) ||
+      !aligned(src_lens, 4) || !aligned(base, 4) || !aligned(weights, 4) || !aligned(workspace, 256))
+    return MLA_ERR_INVALID_ARG;
+  const size_t need = mla_compact_workspace_bytes(shape, max_rows);
+  if (need == 0) return MLA_ERR_UNSUPPORTED;
+  if (workspace_bytes < need) return MLA_ERR_WORKSPACE;
+  int sms = 0;
+  if ((rc = device_sms(&sms)) != MLA_OK) return rc;
+  return launch_compact(shape, kv_cache, kv_scale, block_table, src, src_lens, base, max_rows, weights, workspace, sms,
+                        static_cast<cudaStream_t>(stream), test_stall);
 }
 
 }  // namespace
@@ -646,21 +666,19 @@ int mla_cache_compact(const mla_shape_t* shape, void* kv_cache, float* kv_scale,
                       const int32_t* src, const int32_t* src_lens, const int32_t* base, int32_t max_rows, float* weights,
                       void* workspace, size_t workspace_bytes, void* stream) {
   CallRange range_("mla_cache_compact");
-  int rc = check_shape(shape);
-  if (rc != MLA_OK) return rc;
-  if (!kv_cache || !block_table || !src || !src_lens || !workspace || max_rows < 1) return MLA_ERR_INVALID_ARG;
-  if (shape->cache_dtype == MLA_CACHE_FP8_E4M3 && !kv_scale) return MLA_ERR_INVALID_ARG;
-  if (!aligned(kv_cache, 256) || !aligned(kv_scale, 4) || !aligned(block_table, 4) || !aligned(src, 4) ||
-      !aligned(src_lens, 4) || !aligned(base, 4) || !aligned(weights, 4) || !aligned(workspace, 256))
-    return MLA_ERR_INVALID_ARG;
-  const size_t need = mla_compact_workspace_bytes(shape, max_rows);
-  if (need == 0) return MLA_ERR_UNSUPPORTED;
-  if (workspace_bytes < need) return MLA_ERR_WORKSPACE;
-  int sms = 0;
-  if ((rc = device_sms(&sms)) != MLA_OK) return rc;
-  return launch_compact(shape, kv_cache, kv_scale, block_table, src, src_lens, base, max_rows, weights, workspace, sms,
-                        static_cast<cudaStream_t>(stream));
+  return cache_compact(shape, kv_cache, kv_scale, block_table, src, src_lens, base, max_rows, weights, workspace,
+                       workspace_bytes, stream, 0);
 }
+
+#ifdef MLA_TEST_ENTRY_POINTS
+// Test-only entry point: mla_cache_compact with the kernel's stall hook set.
+int mla_test_compact_stalled(const mla_shape_t* shape, void* kv_cache, float* kv_scale, const int32_t* block_table,
+                             const int32_t* src, const int32_t* src_lens, const int32_t* base, int32_t max_rows,
+                             float* weights, void* workspace, size_t workspace_bytes, void* stream) {
+  return cache_compact(shape, kv_cache, kv_scale, block_table, src, src_lens, base, max_rows, weights, workspace,
+                       workspace_bytes, stream, 1);
+}
+#endif
 
 int mla_compact_get_device_status(void* workspace, void* stream, int* status) {
   return read_status_word(workspace, stream, status);

@@ -53,6 +53,7 @@ struct CompArgs {
   float* weights;
   uint32_t* ws;
   int batch, groups, max_rows, max_pages, num_pages;
+  int test_stall;   // 0 in every product call; 1: nobody learns that a request's first group has been read
 };
 
 // Byte offset of piece `ch` of row `slot` (page * 64 + place) in the pool.
@@ -210,7 +211,7 @@ __global__ void __launch_bounds__(kCompThreads, kCompCtas) compact_kernel(const 
     next_moves = __syncthreads_or(next_moves || zero != 0u) != 0;   // the CTA's rows have been read
     bool ok = true;
     if (exists && !solo) {
-      if (tid == 0) st_release(flags + g, epoch);
+      if (tid == 0 && !(a.test_stall != 0 && g == 0)) st_release(flags + g, epoch);
       if (waits && !ready_sh[b]) {
         if (tid <= g1 - g0) {
           uint64_t t0, t1;
@@ -266,11 +267,11 @@ size_t compact_workspace_bytes(const mla_shape_t* shape, int max_rows) {
 
 int launch_compact(const mla_shape_t* shape, void* kv, float* kv_scale, const int32_t* block_table, const int32_t* src,
                    const int32_t* src_lens, const int32_t* base, int max_rows, float* weights, void* ws, int num_sms,
-                   cudaStream_t stream) {
+                   cudaStream_t stream, int test_stall) {
   const bool fp8 = shape->cache_dtype == MLA_CACHE_FP8_E4M3;
   const int groups = groups_for(fp8, max_rows);
   CompArgs a{static_cast<uint8_t*>(kv), kv_scale, block_table, src, src_lens, base, weights, static_cast<uint32_t*>(ws),
-             shape->batch, groups, max_rows, shape->max_pages_per_seq, shape->num_pages};
+             shape->batch, groups, max_rows, shape->max_pages_per_seq, shape->num_pages, test_stall};
   // as many CTAs as are resident, in whole rounds of the requests (a CTA then
   // stays with one); where no CTA waits for another, one each
   const int64_t total = int64_t(shape->batch) * groups;

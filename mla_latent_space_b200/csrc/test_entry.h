@@ -39,6 +39,15 @@ int mla_test_attn_weights_stalled(const mla_shape_t* shape, const void* q, const
                                   float softmax_scale, float decay, float* weights, void* workspace,
                                   size_t workspace_bytes, void* stream);
 
+/* mla_cache_compact with its kernel's test hook set: the groups whose rows
+ * go where rows of a request's first group lay are never told that those
+ * have been read; their waits run out after about 2 s each.
+ * mla_compact_get_device_status then reports MLA_ERR_TIMEOUT and the rows of
+ * those requests are not valid.  Faults nothing. */
+int mla_test_compact_stalled(const mla_shape_t* shape, void* kv_cache, float* kv_scale, const int32_t* block_table,
+                             const int32_t* src, const int32_t* src_lens, const int32_t* base, int32_t max_rows,
+                             float* weights, void* workspace, size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -353,3 +353,32 @@ def test_compact_in_many_rounds(cache, b, rows, t, kind):
         assert comp.status() == 0
         assert torch.equal(bits(pool), bits(p_ref)) and torch.equal(w, w_ref)
         assert sc is None or torch.equal(sc, s_ref)
+
+
+@pytest.mark.parametrize("cache", ["bf16", "fp8"])
+def test_a_compaction_whose_wait_runs_out_says_so_and_the_next_one_is_right(cache):
+    """The test library's stalled call never says that a request's first group has been read: after 2 s the group
+    that waits for it reports that, leaves its rows alone and the kernel ends."""
+    import ctypes
+    import time
+    from gpu_helpers import test_lib
+    fn = test_lib().mla_test_compact_stalled
+    fn.argtypes, fn.restype = mla.lib().mla_cache_compact.argtypes, ctypes.c_int
+    wl = mw.make(2, 1, 1, [300, 300], seed=19, cache_dtype=cache)
+    src = np.full((2, 200), -1, dtype=np.int32)
+    src[0] = np.arange(1, 201)                          # the second group's first row goes where the first group's last lay
+    src[1, :10] = np.arange(50, 60)
+    lens = np.array([200, 10], dtype=np.int32)
+    comp = mla.CacheCompactor(mla.make_shape(2, 1, 1, wl.max_pages, wl.num_pages, cache), 200)
+    pool, sc = wl.pool.cuda(), None if wl.kv_scale is None else wl.kv_scale.cuda()
+    bt, s_d, l_d = torch.from_numpy(wl.block_table).cuda(), torch.from_numpy(src).cuda(), torch.from_numpy(lens).cuda()
+    torch.cuda.synchronize()
+    t0 = time.perf_counter()
+    assert fn(ctypes.byref(comp.shape), pool.data_ptr(), None if sc is None else sc.data_ptr(), bt.data_ptr(), s_d.data_ptr(),
+              l_d.data_ptr(), None, 200, None, comp.workspace.data_ptr(), comp.workspace.numel(),
+              torch.cuda.current_stream().cuda_stream) == 0
+    torch.cuda.synchronize()
+    assert 1.0 < time.perf_counter() - t0 < 30.0
+    assert comp.status() == -5 and comp.status() == 0
+    check_compact(wl, src, lens, comp=comp)             # the same workspace, a cache that has not moved
+    check_compact(wl, src, lens, comp=comp)
