@@ -322,7 +322,11 @@ int mla_tree_mask(int32_t batch, int32_t s_q, const int32_t* parents, const int3
  *   weights[r][j] = decay * weights[r][j]
  *                 + sum over (i, h), token i seeing j, of
  *                   exp(softmax_scale * q[r][i][h] . C_j - lse[r][i][h])
- * for j < seqlens[r]; later entries are left as they were.  Which positions
+ * for j < seqlens[r]; later entries are left as they were.  An entry behind
+ * the length therefore keeps what its last token left there (a rejected node's
+ * weight, or after a compaction a moved or evicted token's): before the first
+ * call that covers a newly appended token j the caller sets weights[r][j] to 0
+ * (or to the weight that the token is to start with).  Which positions
  * query token i sees is the shape's causal rule (mla_decode_fwd).  lse is the
  * decode's output for the same q, cache and scale.  A row whose lse is -inf
  * adds nothing, whatever its q holds (so padded query tokens can be marked;
@@ -380,7 +384,9 @@ int mla_evict_select(int32_t batch, int32_t max_tokens, const float* weights, co
  *             not moved and flagged; the request's rows are then not valid.
  *   src_lens: int32 [batch]; outside [0, max_rows]: clamped and flagged.
  *   base    : int32 [batch] or NULL.  Negative: flagged, nothing moved.
- *   weights : fp32 [batch, max_pages_per_seq * 64] or NULL; moved as the rows.
+ *   weights : fp32 [batch, max_pages_per_seq * 64] or NULL; moved as the rows
+ *             (and, as the rows, left as they were from the new length on: see
+ *             mla_attn_weights_fwd for what that asks of an appended token).
  *   kv_scale: FP8 cache: moved as the rows.
  *   workspace: mla_compact_workspace_bytes(shape, max_rows) bytes, 256-byte
  *             aligned, zero-filled before its first use; calls that may

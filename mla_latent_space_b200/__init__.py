@@ -434,7 +434,9 @@ class AttnWeights:
                    stream=None):
         """weights[r, j] = decay * weights[r, j] + the attention weight that
         the rows of q give cached token j (lse: the decode's output).  weights
-        fp32 [b, max_pages * 64], updated in place."""
+        fp32 [b, max_pages * 64], updated in place.  The entry of a token that
+        was appended since the last call must have been set to 0 (it still
+        holds what the place's last token left there)."""
         sh, dev = self.shape, torch.cuda.current_device()
         b, s, h = sh.batch, sh.s_q, sh.num_heads
         _need_here(dev, q, "q", torch.bfloat16, (b, s, h, D_QK))

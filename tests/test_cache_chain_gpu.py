@@ -152,3 +152,60 @@ def test_pools_past_four_gigabytes(cache):
     if sc is not None:
         assert torch.equal(sc[far:].cpu(), s_ref)
     assert tree.status() == 0 and acc.status() == 0 and comp.status() == 0
+
+
+def test_a_loop_that_appends_weighs_and_evicts_follows_every_token_by_name():
+    """Decode, weigh, append, cut, and again: each token's weight is that of the token, wherever its row lies by then.
+
+    A term is within 3e-4 of itself given the lse (see the weights' tests), so a sum of them is; each step rounds the
+    sum once more.
+    """
+    b, h, budget, cap, steps = 3, 16, 70, 96, 60
+    wl = mw.make(b, 1, h, [cap] * b, seed=120)
+    g = torch.Generator().manual_seed(121)
+    pages = wl.max_pages
+    bt, pool = torch.from_numpy(wl.block_table).cuda(), wl.pool.cuda()
+    n = np.array([80, 33, 64])
+    rows = [[wl.pool[wl.block_table[r, j // 64], j % 64].double().numpy() for j in range(n[r])] for r in range(b)]
+    model = [[0.0] * n[r] for r in range(b)]            # by token, as rows
+    w = torch.zeros((b, pages * 64), device="cuda")
+    shape = mla.make_shape(b, 1, h, pages, wl.num_pages)
+    dec, acc, comp = mla.Decoder(shape), mla.AttnWeights(shape), mla.CacheCompactor(shape, budget)
+    kept = torch.empty((b, budget), dtype=torch.int32, device="cuda")
+    n_kept = torch.empty(b, dtype=torch.int32, device="cuda")
+    out = torch.empty((b, 1, h, 512), dtype=torch.bfloat16, device="cuda")
+    lse = torch.empty((b, 1, h), device="cuda")
+    evictions = stale = 0
+    for step in range(steps):
+        q = torch.randn((b, 1, h, 576), generator=g).bfloat16()
+        sl = torch.from_numpy(n.astype(np.int32)).cuda()
+        dec.schedule(sl)
+        dec.decode(q.cuda(), pool, None, bt, sl, wl.softmax_scale, out, lse)
+        acc.accumulate(q.cuda(), pool, bt, sl, lse, wl.softmax_scale, 0.9, w)
+        got, l_now = w.cpu().numpy().astype(np.float64), lse.cpu().numpy().astype(np.float64)
+        for r in range(b):
+            x = np.stack(rows[r]) @ q[r, 0].double().numpy().T * wl.softmax_scale
+            new = np.exp(x - l_now[r, 0]).sum(1)
+            model[r] = [0.9 * a + c for a, c in zip(model[r], new)]
+            ref = np.array(model[r])
+            assert (np.abs(got[r, :n[r]] - ref) <= (3e-4 + steps * 2.0 ** -23) * ref).all(), (step, r)
+        if (n >= cap - 1).any():                        # cut all to the budget
+            mla.mla_evict_select(w, sl, budget, 4, 16, kept, n_kept)
+            k_ref, n_ref = oracle.evict_select(w.cpu().numpy(), n, budget, 4, 16)
+            assert np.array_equal(kept.cpu().numpy(), k_ref) and np.array_equal(n_kept.cpu().numpy(), n_ref)
+            comp.compact(pool, bt, kept, n_kept, weights=w)
+            for r in range(b):
+                rows[r] = [rows[r][j] for j in k_ref[r, :n_ref[r]]]
+                model[r] = [model[r][j] for j in k_ref[r, :n_ref[r]]]
+            n = n_ref.astype(np.int64)
+            evictions += 1
+        for r in range(b):                              # append a token: its row, and a weight of zero
+            row = torch.randn(576, generator=g).bfloat16()
+            pool[wl.block_table[r, n[r] // 64], n[r] % 64] = row.cuda()
+            stale += int(w[r, n[r]] != 0)
+            w[r, n[r]] = 0.0
+            rows[r].append(row.double().numpy())
+            model[r].append(0.0)
+        n = n + 1
+    assert evictions >= 2 and stale > 0                 # places were used again, with something in them
+    assert dec.status() == 0 and acc.status() == 0 and comp.status() == 0
