@@ -364,7 +364,7 @@ int mla_attn_weights_get_device_status(void* workspace, void* stream, int* statu
  *             2^24, max_tokens and budget <= 2^30.
  *   kept    : int32 [batch, budget], the kept positions in ascending order,
  *             then -1 (the form of mla_sparse_decode_fwd's lists).
- *   kept_lens: int32 [batch], min(seqlens[r], budget).
+ *   kept_lens: int32 [batch], min(seqlens[r], budget); may be seqlens itself.
  *   device_status: optional device int32 that a length out of range ORs a
  *             nonzero bit into (never cleared by this call). */
 int mla_evict_select(int32_t batch, int32_t max_tokens, const float* weights, const int32_t* seqlens, int32_t budget,

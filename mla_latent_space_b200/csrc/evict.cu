@@ -69,9 +69,8 @@ __device__ __forceinline__ int warp_prefix(const int* sums, int warp, int lane) 
 
 template <int kCtas, bool kInSmem>
 __global__ void __launch_bounds__(kSelThreads)
-evict_select_kernel(const float* __restrict__ weights, int max_tokens, const int32_t* __restrict__ seqlens, int budget,
-                    int sink, int recent, int32_t* __restrict__ kept, int32_t* __restrict__ kept_lens,
-                    int32_t* __restrict__ status) {
+evict_select_kernel(const float* __restrict__ weights, int max_tokens, const int32_t* seqlens, int budget, int sink,
+                    int recent, int32_t* __restrict__ kept, int32_t* kept_lens, int32_t* __restrict__ status) {
   extern __shared__ uint32_t keys[];
   __shared__ SelShared sh;
   const int r = blockIdx.x / kCtas, rank = blockIdx.x % kCtas;
@@ -83,8 +82,10 @@ evict_select_kernel(const float* __restrict__ weights, int max_tokens, const int
   }
   const float* w = weights + size_t(r) * size_t(max_tokens);
   int32_t* out = kept + size_t(r) * size_t(budget);
-  if (rank == 0 && tid == 0) kept_lens[r] = min(t, budget);
+  // kept_lens may be seqlens: it is written where every thread has read the
+  // length, or where what is written is the length
   if (t <= budget) {   // (every CTA of the cluster agrees)
+    if (rank == 0 && tid == 0) kept_lens[r] = t;
     for (int k = rank * kSelThreads + tid; k < budget; k += kCtas * kSelThreads) out[k] = k < t ? k : -1;
     return;
   }
@@ -197,6 +198,8 @@ evict_select_kernel(const float* __restrict__ weights, int max_tokens, const int
     }
     shift -= pass == 0 ? 11 : 10;
   }
+
+  if (rank == 0 && tid == 0) kept_lens[r] = budget;   // (a pass has met all threads of the row)
 
   // ordered output: warp `warp` owns a contiguous run of the chunk
   const int run = (n32 / 32 + kSelWarps - 1) / kSelWarps * 32;

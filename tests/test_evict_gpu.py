@@ -382,3 +382,15 @@ def test_a_compaction_whose_wait_runs_out_says_so_and_the_next_one_is_right(cach
     assert comp.status() == -5 and comp.status() == 0
     check_compact(wl, src, lens, comp=comp)             # the same workspace, a cache that has not moved
     check_compact(wl, src, lens, comp=comp)
+
+
+@pytest.mark.parametrize("T,b", [(200, 5), (3000, 40), (20000, 9), (60000, 40), (400000, 2)])
+def test_select_updates_the_lengths_in_place(T, b):
+    # kept_lens may be seqlens: one CTA a request, clusters, and rows that are re-read
+    w = weights(b, T, T + b)
+    seqlens = [[T, T // 2, 60, 0, T - 1, -5, T + 9][r % 7] for r in range(b)]
+    dev, sl = torch.from_numpy(w).cuda(), torch.tensor(seqlens, dtype=torch.int32, device="cuda")
+    kept = torch.full((b, 100), 77, dtype=torch.int32, device="cuda")
+    mla.mla_evict_select(dev, sl, 100, 4, 16, kept, sl)
+    k_ref, l_ref = oracle.evict_select(w, seqlens, 100, 4, 16)
+    assert np.array_equal(sl.cpu().numpy(), l_ref) and np.array_equal(kept.cpu().numpy(), k_ref)
