@@ -392,9 +392,11 @@ class TreeDecoder:
         _check(rc, "mla_tree_decode_fwd")
 
     def status(self, stream=None) -> int:
+        dev = torch.cuda.current_device()
+        _need_here(dev, self.workspace, "the decoder's workspace", torch.uint8)
         st = ctypes.c_int(0)
         _check(lib().mla_tree_get_device_status(ctypes.byref(self.shape), self.n_sms, _ptr(self.workspace),
-                                                _stream(stream), ctypes.byref(st)), "mla_tree_get_device_status")
+                                                _stream_of(dev, stream), ctypes.byref(st)), "mla_tree_get_device_status")
         return int(st.value)
 
 
@@ -451,8 +453,10 @@ class AttnWeights:
         _check(rc, "mla_attn_weights_fwd")
 
     def status(self, stream=None) -> int:
+        dev = torch.cuda.current_device()
+        _need_here(dev, self.workspace, "the object's workspace", torch.uint8)
         st = ctypes.c_int(0)
-        _check(lib().mla_attn_weights_get_device_status(_ptr(self.workspace), _stream(stream), ctypes.byref(st)),
+        _check(lib().mla_attn_weights_get_device_status(_ptr(self.workspace), _stream_of(dev, stream), ctypes.byref(st)),
                "mla_attn_weights_get_device_status")
         return int(st.value)
 
@@ -506,8 +510,10 @@ class CacheCompactor:
         _check(rc, "mla_cache_compact")
 
     def status(self, stream=None) -> int:
+        dev = torch.cuda.current_device()
+        _need_here(dev, self.workspace, "the object's workspace", torch.uint8)
         st = ctypes.c_int(0)
-        _check(lib().mla_compact_get_device_status(_ptr(self.workspace), _stream(stream), ctypes.byref(st)),
+        _check(lib().mla_compact_get_device_status(_ptr(self.workspace), _stream_of(dev, stream), ctypes.byref(st)),
                "mla_compact_get_device_status")
         return int(st.value)
 

@@ -186,3 +186,22 @@ def test_plain_schedule_is_unchanged_by_the_tree_fields():
     sc = _schedule(None, [100, 300], 16, 128)
     tiles = sc[16 + 74 * 8:].view(-1, 4)
     assert tiles[:16, 0].tolist() == [2] * 16 and tiles[16:32, 0].tolist() == [5] * 16
+
+
+@pytest.mark.parametrize("cls", ["TreeDecoder", "AttnWeights", "CacheCompactor"])
+def test_status_is_read_on_the_device_that_ran_the_calls(monkeypatch, cls):
+    # on another device's stream the read would not wait for the calls
+    class On(torch.Tensor):
+        def get_device(self):
+            return 1
+
+        @property
+        def is_cuda(self):
+            return True
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(mla, "_stream_of", lambda dev, stream: None)
+    obj = getattr(mla, cls).__new__(getattr(mla, cls))
+    obj.shape, obj.n_sms = shape(), 148
+    obj.workspace = torch.zeros(256, dtype=torch.uint8).as_subclass(On)
+    with pytest.raises(ValueError, match="current device"):
+        obj.status()
