@@ -467,18 +467,20 @@ def mla_evict_select(weights, seqlens, budget, sink, recent, kept, kept_lens,
     last `recent`, the heaviest between), ascending, then -1; kept_lens int32
     [b].  weights fp32 [b, max_tokens]."""
     dev = torch.cuda.current_device()
+    budget, sink, recent = int(budget), int(sink), int(recent)
+    if sink < 0 or recent < 0 or sink + recent > budget:   # (here, as ctypes keeps only the low 32 bits of an int)
+        raise MLAError(-1, "mla_evict_select")
     _need_here(dev, weights, "weights", torch.float32)
     if weights.dim() != 2:
         raise ValueError(f"weights must have shape [batch, max_tokens], got {tuple(weights.shape)}")
     b, max_tokens = weights.shape
     _need_here(dev, seqlens, "seqlens", torch.int32, (b,))
-    _need_here(dev, kept, "kept", torch.int32, (b, int(budget)))
+    _need_here(dev, kept, "kept", torch.int32, (b, budget))
     _need_here(dev, kept_lens, "kept_lens", torch.int32, (b,))
     if device_status is not None:
         _need_here(dev, device_status, "device_status", torch.int32)
-    _check(lib().mla_evict_select(b, max_tokens, _ptr(weights), _ptr(seqlens), int(budget), int(sink), int(recent),
-                                  _ptr(kept), _ptr(kept_lens), _ptr(device_status), _stream_of(dev, stream)),
-           "mla_evict_select")
+    _check(lib().mla_evict_select(b, max_tokens, _ptr(weights), _ptr(seqlens), budget, sink, recent, _ptr(kept),
+                                  _ptr(kept_lens), _ptr(device_status), _stream_of(dev, stream)), "mla_evict_select")
 
 
 class CacheCompactor:

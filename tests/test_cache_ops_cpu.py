@@ -205,3 +205,21 @@ def test_status_is_read_on_the_device_that_ran_the_calls(monkeypatch, cls):
     obj.workspace = torch.zeros(256, dtype=torch.uint8).as_subclass(On)
     with pytest.raises(ValueError, match="current device"):
         obj.status()
+
+
+def test_binding_does_not_let_a_count_wrap_to_32_bits(monkeypatch):
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(mla, "_need_here", lambda *a: None)
+    monkeypatch.setattr(mla, "_stream_of", lambda dev, stream: None)
+    monkeypatch.setattr(mla, "lib", lambda real=mla.lib(): Passes(real))
+
+    class Passes:
+        """The library, but for the choice, which would take what reaches it."""
+        def __init__(self, real):
+            self.mla_error_string = real.mla_error_string
+            self.mla_evict_select = lambda *a: 0
+    w, n, kept = torch.zeros((2, 64)), torch.zeros(2, dtype=torch.int32), torch.zeros((2, 16), dtype=torch.int32)
+    mla.mla_evict_select(w, n, 16, 4, 4, kept, n)
+    for sink, recent in ((2**32, 0), (4, 2**32 + 4), (-1, 0), (0, -2**32), (9, 8)):
+        with pytest.raises(mla.MLAError):
+            mla.mla_evict_select(w, n, 16, sink, recent, kept, n)
