@@ -262,3 +262,44 @@ def test_status_stays_until_it_is_read_and_is_cleared_by_the_read(what):
     assert dec.status() == 0
     step(good, dev["seqlens"])
     assert dec.status() == 0
+
+
+@pytest.mark.parametrize("b,s", [(1, 8193), (3, 8300), (2, 20000)])
+def test_tree_mask_bits_of_large_trees(b, s):
+    par = parents_of(b, s, seed=s)
+    par[0, 5000:] = np.maximum(par[0, 5000:], np.arange(5000, s) - 40)     # deep: parents near their children
+    par[-1, 70], par[-1, 100], par[-1, s - 1] = 70, -9, s                   # bad ones: -1
+    lens = np.array([s - 33 * r for r in range(b)], dtype=np.int32)
+    lens[-1] = s + 1 if b == 2 else lens[-1]                                # a count past the slots
+    m = torch.full((b, s, (s + 63) // 64), -1, dtype=torch.int64, device="cuda")
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    mla.mla_tree_mask(torch.from_numpy(par).cuda(), m, torch.from_numpy(lens).cuda(), st)
+    got = m.cpu().numpy().view(np.uint64)
+    assert st.item() != 0
+    for r in range(b):
+        ref = np.zeros_like(got[r])
+        for i in range(min(s, int(lens[r]))):           # a row is its parent's and the node's own bit
+            p = par[r, i]
+            if 0 <= p < i:
+                ref[i] = ref[p]
+            ref[i, i // 64] |= np.uint64(1) << np.uint64(i % 64)
+        assert np.array_equal(got[r], ref)
+
+
+def test_tree_mask_of_a_long_chain_takes_no_time_worth_mentioning():
+    # time that grows as nodes x words (a walk of every path by every word would take seconds here)
+    s = 131072
+    par = torch.arange(-1, s - 1, dtype=torch.int32, device="cuda")[None]
+    m = torch.full((1, s, s // 64), 77, dtype=torch.int64, device="cuda")
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+    a.record()
+    mla.mla_tree_mask(par, m, None, st)
+    b.record()
+    b.synchronize()
+    assert a.elapsed_time(b) < 1000.0 and st.item() == 0
+    w = torch.arange(s // 64, device="cuda")
+    for i0 in range(0, s, 8192):
+        n = (torch.arange(i0, i0 + 8192, device="cuda")[:, None] + 1 - 64 * w).clamp(0, 64)
+        ref = torch.where(n == 64, -1, (1 << n.clamp(max=63)) - 1)
+        assert torch.equal(m[0, i0:i0 + 8192], ref)
