@@ -237,6 +237,15 @@ int tree_overhead(const mla_shape_t* s) {
   return s->cache_dtype == MLA_CACHE_FP8_E4M3 ? kTreeOverheadFp8 : kTreeOverhead;
 }
 
+// What the tree decode's scheduler plans.
+ShapeInfo tree_info(const mla_shape_t* s, const int32_t* draft_lens) {
+  ShapeInfo si = shape_info(s);
+  si.tree = 1;
+  si.draft_lens = draft_lens;
+  si.overhead = tree_overhead(s);
+  return si;
+}
+
 bool tree_layout(const mla_shape_t* s, int num_sms, TreeLayout* L) {
   if (check_shape(s) != MLA_OK || s->causal != 0 || num_sms < 1) return false;
   const ShapeInfo si = shape_info(s);
@@ -590,10 +599,7 @@ int mla_tree_decode_fwd(const mla_shape_t* shape, const void* q, const void* kv_
   DecodePrepared prep;
   if ((rc = prepare_decode_sm100(shape, q, kv_cache, &prep, true)) != MLA_OK) return rc;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  ShapeInfo si = shape_info(shape);
-  si.tree = 1;
-  si.draft_lens = draft_lens;
-  si.overhead = tree_overhead(shape);
+  ShapeInfo si = tree_info(shape, draft_lens);
   si.sticky = static_cast<int32_t*>(ws);
   if (launch_schedule(seqlens, si, num_workers_for(sms), static_cast<int32_t*>(sched), st) != cudaSuccess)
     return MLA_ERR_CUDA;
@@ -605,6 +611,18 @@ int mla_tree_decode_fwd(const mla_shape_t* shape, const void* q, const void* kv_
   return launch_combine(sched, ws, out, lse, si.batch * si.tiles_per_req, cap, st) == cudaSuccess ? MLA_OK
                                                                                                   : MLA_ERR_CUDA;
 }
+
+#ifdef MLA_TEST_ENTRY_POINTS
+// Test-only entry point: mla_plan_schedule_host for the tree decode.
+int mla_test_plan_tree_schedule_host(const mla_shape_t* shape, const int32_t* seqlens, const int32_t* draft_lens, int num_sms,
+                                     void* sched, size_t sched_bytes) {
+  TreeLayout L;
+  if (!seqlens || !sched || !tree_layout(shape, num_sms, &L)) return MLA_ERR_INVALID_ARG;
+  if (sched_bytes < L.sched_bytes) return MLA_ERR_WORKSPACE;
+  plan_schedule_host(seqlens, tree_info(shape, draft_lens), num_workers_for(num_sms), static_cast<int32_t*>(sched));
+  return MLA_OK;
+}
+#endif
 
 int mla_tree_get_device_status(const mla_shape_t* shape, int num_sms, void* workspace, void* stream, int* status) {
   TreeLayout L;

@@ -39,6 +39,12 @@ int mla_test_attn_weights_stalled(const mla_shape_t* shape, const void* q, const
                                   float softmax_scale, float decay, float* weights, void* workspace,
                                   size_t workspace_bytes, void* stream);
 
+/* The host copy of the tree decode's scheduler (mla_plan_schedule_host for
+ * mla_tree_decode_fwd's schedule, which lies at the head of its workspace):
+ * seqlens, draft_lens (or NULL) and sched are HOST pointers. */
+int mla_test_plan_tree_schedule_host(const mla_shape_t* shape, const int32_t* seqlens, const int32_t* draft_lens, int num_sms,
+                                     void* sched, size_t sched_bytes);
+
 /* mla_cache_compact with its kernel's test hook set: the groups whose rows
  * go where rows of a request's first group lay are never told that those
  * have been read; their waits run out after about 2 s each.

@@ -303,3 +303,35 @@ def test_tree_mask_of_a_long_chain_takes_no_time_worth_mentioning():
         n = (torch.arange(i0, i0 + 8192, device="cuda")[:, None] + 1 - 64 * w).clamp(0, 64)
         ref = torch.where(n == 64, -1, (1 << n.clamp(max=63)) - 1)
         assert torch.equal(m[0, i0:i0 + 8192], ref)
+
+
+@pytest.mark.parametrize("cache", ["bf16", "fp8"])
+@pytest.mark.parametrize("b,s,heads,top", [(8, 6, 40, 9000), (40, 24, 16, 3000), (300, 3, 16, 500), (4000, 20, 16, 64),
+                                           (26000, 1, 1, 128)])
+def test_the_device_plans_what_the_host_plans(cache, b, s, heads, top):
+    # the last two: more tiles than the default shared memory holds (about 6000), and more than any (about 25500)
+    from schedule_plan import plan, tree_host
+    g = np.random.default_rng(b)
+    lengths = np.exp(g.uniform(0, np.log(top + 1), b)).astype(np.int32)
+    lengths[0], lengths[-1] = top, 0
+    counts = g.integers(0, s + 2, b).astype(np.int32)                  # some past what the length allows: flagged
+    pages = -(-top // 64)
+    sh = mla.make_shape(b, s, heads, pages, 4, cache)
+    dec = mla.TreeDecoder(sh)
+    q = torch.zeros((b, s, heads, 576), dtype=torch.bfloat16, device="cuda")
+    pool = torch.zeros((4, 64, 576), dtype=torch.bfloat16, device="cuda") if cache == "bf16" else \
+        torch.zeros((4, 40960), dtype=torch.uint8, device="cuda")
+    sc = None if cache == "bf16" else torch.ones((4, 64), device="cuda")
+    bt = torch.zeros((b, pages), dtype=torch.int32, device="cuda")
+    mask = torch.full((b, s, 1), -1, dtype=torch.int64, device="cuda")
+    out = torch.empty((b, s, heads, 512), dtype=torch.bfloat16, device="cuda")
+    lse = torch.empty((b, s, heads), device="cuda")
+    for dl in (counts, None):
+        dec.decode(q, pool, bt, torch.from_numpy(lengths).cuda(), mask, 0.1, out, lse, kv_scale=sc,
+                   draft_lens=None if dl is None else torch.from_numpy(dl).cuda())
+        ref = tree_host(sh, lengths, dl, dec.n_sms)
+        assert np.array_equal(dec.workspace[:ref.nbytes].cpu().numpy().view(np.int32), ref)
+        assert (dec.status() == -6) == (ref[6] != 0) and (ref[6] != 0) == (dl is not None)
+        n = np.minimum(lengths, s) if dl is None else np.clip(dl, 0, np.minimum(lengths, s))
+        live = lse.isfinite().view(b, s, heads).all(2).sum(1).cpu().numpy()
+        assert np.array_equal(live, n)
