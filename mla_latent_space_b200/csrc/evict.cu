@@ -16,10 +16,21 @@
 // is one CTA's work, or it is cut into contiguous chunks over a cluster of 8
 // CTAs, which add up each other's histograms and counts over distributed
 // shared memory.  Rows too long even for that re-read the weights through L2
-// in every pass.  The cluster pays for long rows in small batches (us, one
-// CTA / cluster; batches of 4, 32, 64: 8192 tokens 13 / 14, - , 13 / 27;
-// 32768 tokens 25 / 15, 25 / 18, 25 / 32; 49152 tokens at 32: 33 / 20).  What bounds it is
-// latency: of the 16 us of two rows of 131072 tokens, 3.5 are the trip to
+// in every pass.  The cluster pays for long rows as long as the clusters of
+// all rows run at once, two CTAs an SM (us, one CTA / cluster; a row is full):
+//
+//   tokens   batch 2       8         16        32        33        37        64
+//    4096    8 / 10      8 / 11    8 / 11    8 / 13    8 / 13    8 / 18    9 / 22
+//   10000   11 / 11     11 / 12   11 / 13   11 / 15   11 / 15   11 / 20   11 / 24
+//   16384   13 / 11     13 / 11   13 / 13   13 / 15   13 / 15   13 / 20   14 / 26
+//   24576   15 / 11     15 / 11   18 / 14   18 / 16   18 / 17   17 / 22   18 / 28
+//   32768   22 / 13     20 / 12   22 / 15   22 / 15   22 / 17   22 / 24   22 / 28
+//   49152   26 / 12     28 / 13   28 / 16   28 / 20   28 / 19   28 / 25   28 / 32
+//
+// so a row is one CTA's up to 8192 tokens and 400 more for each row of the
+// batch, or where the clusters would queue.  The host knows the rows' length,
+// not the requests': 64 requests of 4096 tokens in rows of 131072, which only
+// a cluster holds, take 22 us.  What bounds it is latency: of the 16 us of two rows of 131072 tokens, 3.5 are the trip to
 // memory, 5 the digits' passes with their cluster barriers, 5 the ordered
 // output.  (Adding up equal bins within a warp before the shared-memory adds,
 // for the many weights that are zero, costs more than it saves: 30.7 us
@@ -40,8 +51,8 @@ constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kBins = 2048;
 constexpr int kPasses = 3;
 constexpr int kCluster = 8;
-constexpr int kWideTokens = 8192;            // up to here, or in batches above kWideBatch, one CTA a row
-constexpr int kWideBatch = 32;
+constexpr int kWideTokens = 8192;            // up to here, and kWidePerRow more for each row, one CTA a row
+constexpr int kWidePerRow = 400;
 constexpr int kSmemKeys = 48 * 1024;         // keys per CTA that fit beside the histograms (192 KB)
 
 struct alignas(16) SelShared {
@@ -276,10 +287,47 @@ cudaError_t launch(const float* weights, int max_tokens, const int32_t* seqlens,
 
 }  // namespace
 
+namespace {
+
+// Clusters that run at once on the current device, of rows of up to kSmemKeys
+// tokens (an eighth of the keys and the histograms a CTA); 0 if unknown.
+int resident_clusters() {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+  static std::mutex mu;
+  static int cache[64] = {};   // + 1
+  std::lock_guard<std::mutex> lock(mu);
+  if (cache[dev] == 0) {
+    auto fn = &evict_select_kernel<kCluster, true>;
+    if (!ensure_smem_attr(reinterpret_cast<const void*>(fn), kSmemKeys * 4)) return 0;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(kCluster);
+    cfg.blockDim = dim3(kSelThreads);
+    cfg.dynamicSmemBytes = kSmemKeys / kCluster * 4;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = kCluster;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, fn, &cfg) != cudaSuccess) {
+      cudaGetLastError();
+      return 0;
+    }
+    cache[dev] = n + 1;
+  }
+  return cache[dev] - 1;
+}
+
+}  // namespace
+
 cudaError_t launch_evict_select(const float* weights, int max_tokens, const int32_t* seqlens, int batch, int budget,
                                 int sink, int recent, int32_t* kept, int32_t* kept_lens, int32_t* status,
                                 cudaStream_t stream) {
-  const bool one = max_tokens <= kWideTokens || (batch > kWideBatch && max_tokens <= kSmemKeys);
+  const bool one = max_tokens <= kSmemKeys &&
+                   (max_tokens <= kWideTokens + int64_t(kWidePerRow) * batch || batch > resident_clusters());
   const auto fn = one                                   ? &launch<1, true>
                   : max_tokens <= kCluster * kSmemKeys ? &launch<kCluster, true>
                                                          : &launch<kCluster, false>;

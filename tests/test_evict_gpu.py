@@ -394,3 +394,10 @@ def test_select_updates_the_lengths_in_place(T, b):
     mla.mla_evict_select(dev, sl, 100, 4, 16, kept, sl)
     k_ref, l_ref = oracle.evict_select(w, seqlens, 100, 4, 16)
     assert np.array_equal(sl.cpu().numpy(), l_ref) and np.array_equal(kept.cpu().numpy(), k_ref)
+
+
+@pytest.mark.parametrize("b,T", [(2, 8900), (2, 9100), (33, 21000), (33, 21600), (32, 49152), (36, 49152), (37, 49152), (37, 49200)])
+def test_select_on_either_side_of_the_choice_of_variant(b, T):
+    w = weights(b, T, b + T)
+    w[1::2] = weights(len(w[1::2]), T, b, "ties")
+    check_select(w, [T - 5 * r for r in range(b)], 2000, 4, 100)
