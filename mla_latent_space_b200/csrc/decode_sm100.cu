@@ -353,6 +353,17 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   return *reinterpret_cast<uint32_t*>(&h);
 }
 
+// Rows of a tile from which on the epilogue's lanes swap their pieces before
+// they store them.  A row's 16-byte stores hold O, and with it the next
+// piece's PVs: for 18 us of 118 at 384 rows a request (b=32, up to 8192
+// tokens, 16 heads), for 8 us swapped.  But the shuffles are on the way of a
+// tile whose few stores nothing waits for.  Stored as they are / swapped, us
+// a step (t=512; 1, 70 and 256 requests) of 32 rows 23.6 / 25.4, 28.9 / 30.1,
+// 76 / 78; 64 rows 24.8 / 25.5, 29.3 / 30.1, 78 / 79; 96 rows 27.0 / 26.0,
+// 30.9 / 29.9, 82 / 79; 128 rows 27.8 / 25.6, 32.1 / 30.0, 88 / 80; the
+// two-term output, 256 requests, 32 rows 139 / 156, 128 rows 195 / 170.
+constexpr int kSwapRows = 96;
+
 // 4 x 4 transpose over four neighbouring lanes: lane q's a[c] goes to lane c's
 // a[q].
 __device__ __forceinline__ void transpose4(uint4 (&a)[4], int lane) {
@@ -1145,70 +1156,104 @@ decode_sm100_kernel(const __grid_constant__ CUtensorMap pool_map, const __grid_c
           const bool whole = sv.tile_splits(pc.T) == 1;
           const int slot = whole ? 0 : sv.tile_slot_base(pc.T) + pc.split;
           const bool slot_ok = whole || slot < p.cap_slots;
-          // Four lanes swap their 16-byte pieces so that a store covers 64
-          // bytes of 8 rows, not 16 bytes of 32: the stores held O, and with
-          // it the next piece's PVs, for 18 us of 118 at 384 rows a request
-          // (b=32, up to 8192 tokens, 16 heads), for 8 us this way.
-          // A warp with rows to skip stores them as they are (16 rows of
-          // 128: 24.5 against 22.5 us a launch).
-          const int rows_here = rows_total - qt * MLA_TILE_ROWS - 32 * wq;   // of this warp's 32
-          auto put = [&](char* tile, size_t row_bytes, uint32_t col, uint4 (&v4)[4]) {
-            if (rows_here >= 32) {
+          const int tile_rows = rows_total - qt * MLA_TILE_ROWS;   // (128 of them at most)
+          const int rows_here = tile_rows - 32 * wq;               // of this warp's 32
+          const size_t row0 = size_t(r) * rows_total + size_t(qt) * MLA_TILE_ROWS;
+          __nv_bfloat16* tile_b = p.out + row0 * MLA_D_V;
+          __nv_bfloat16* tile_l = p.out_lo != nullptr ? p.out_lo + row0 * MLA_D_V : nullptr;
+          float* tile_f = slot_ok && !whole ? ws_partial_o(p.ws, p.cap_slots, slot) : nullptr;
+          if (tile_rows >= kSwapRows && rows_here >= 32) {
+            // four lanes swap their 16-byte pieces so that a store covers 64
+            // bytes of 8 rows, not 16 bytes of 32
+            auto put = [&](void* tile, size_t row_bytes, uint32_t col, uint4 (&v4)[4]) {
               transpose4(v4, lane);
-              char* at = tile + size_t(i & ~3) * row_bytes + col + 16u * uint32_t(lane & 3);
+              char* at = static_cast<char*>(tile) + size_t(i & ~3) * row_bytes + col + 16u * uint32_t(lane & 3);
 #pragma unroll
               for (int u = 0; u < 4; ++u) *reinterpret_cast<uint4*>(at + size_t(u) * row_bytes) = v4[u];
-            } else if (lane < rows_here) {
-#pragma unroll
-              for (int u = 0; u < 4; ++u) *reinterpret_cast<uint4*>(tile + size_t(i) * row_bytes + col + 16u * u) = v4[u];
-            }
-          };
-          const size_t row0 = size_t(r) * rows_total + size_t(qt) * MLA_TILE_ROWS;
-          char* dst_b = reinterpret_cast<char*>(p.out + row0 * MLA_D_V);
-          char* dst_l = p.out_lo != nullptr ? reinterpret_cast<char*>(p.out_lo + row0 * MLA_D_V) : nullptr;
-          char* dst_f = slot_ok && !whole ? reinterpret_cast<char*>(ws_partial_o(p.ws, p.cap_slots, slot)) : nullptr;
+            };
 #pragma unroll 1
-          for (int c = 0; c < 16; ++c) {
-            uint32_t o[32];
-            tmem_ld32(tmem + lane_off + 32u * c, o);
-            tmem_wait_ld();
-            if (!slot_ok || rows_here <= 0) continue;
-            if (whole && p.out_lo == nullptr) {
-              uint4 v4[4];
-#pragma unroll
-              for (int u = 0; u < 4; ++u)
-                v4[u] = make_uint4(
-                    pack_bf16(__uint_as_float(o[8 * u + 0]) * inv, __uint_as_float(o[8 * u + 1]) * inv),
-                    pack_bf16(__uint_as_float(o[8 * u + 2]) * inv, __uint_as_float(o[8 * u + 3]) * inv),
-                    pack_bf16(__uint_as_float(o[8 * u + 4]) * inv, __uint_as_float(o[8 * u + 5]) * inv),
-                    pack_bf16(__uint_as_float(o[8 * u + 6]) * inv, __uint_as_float(o[8 * u + 7]) * inv));
-              put(dst_b, 2 * MLA_D_V, 64u * c, v4);
-            } else if (whole) {
-              // two-term output: hi = bf16(x), lo = bf16(x - hi)
-              uint4 v4[4], l4[4];
-#pragma unroll
-              for (int u = 0; u < 4; ++u) {
-                uint32_t hi[4], lo[4];
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                  split_bf16(__uint_as_float(o[8 * u + 2 * k]) * inv, __uint_as_float(o[8 * u + 2 * k + 1]) * inv,
-                             &hi[k], &lo[k]);
-                v4[u] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                l4[u] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-              }
-              put(dst_b, 2 * MLA_D_V, 64u * c, v4);
-              put(dst_l, 2 * MLA_D_V, 64u * c, l4);
-            } else {
-#pragma unroll
-              for (int half = 0; half < 2; ++half) {
+            for (int c = 0; c < 16; ++c) {
+              uint32_t o[32];
+              tmem_ld32(tmem + lane_off + 32u * c, o);
+              tmem_wait_ld();
+              if (!slot_ok) continue;
+              if (whole && tile_l == nullptr) {
                 uint4 v4[4];
 #pragma unroll
                 for (int u = 0; u < 4; ++u)
-                  v4[u] = make_uint4(__float_as_uint(__uint_as_float(o[16 * half + 4 * u + 0]) * inv),
-                                     __float_as_uint(__uint_as_float(o[16 * half + 4 * u + 1]) * inv),
-                                     __float_as_uint(__uint_as_float(o[16 * half + 4 * u + 2]) * inv),
-                                     __float_as_uint(__uint_as_float(o[16 * half + 4 * u + 3]) * inv));
-                put(dst_f, 4 * MLA_D_V, 128u * c + 64u * half, v4);
+                  v4[u] = make_uint4(
+                      pack_bf16(__uint_as_float(o[8 * u + 0]) * inv, __uint_as_float(o[8 * u + 1]) * inv),
+                      pack_bf16(__uint_as_float(o[8 * u + 2]) * inv, __uint_as_float(o[8 * u + 3]) * inv),
+                      pack_bf16(__uint_as_float(o[8 * u + 4]) * inv, __uint_as_float(o[8 * u + 5]) * inv),
+                      pack_bf16(__uint_as_float(o[8 * u + 6]) * inv, __uint_as_float(o[8 * u + 7]) * inv));
+                put(tile_b, 2 * MLA_D_V, 64u * c, v4);
+              } else if (whole) {
+                // two-term output: hi = bf16(x), lo = bf16(x - hi)
+                uint4 v4[4], l4[4];
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                  uint32_t hi[4], lo[4];
+#pragma unroll
+                  for (int k = 0; k < 4; ++k)
+                    split_bf16(__uint_as_float(o[8 * u + 2 * k]) * inv, __uint_as_float(o[8 * u + 2 * k + 1]) * inv,
+                               &hi[k], &lo[k]);
+                  v4[u] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                  l4[u] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                }
+                put(tile_b, 2 * MLA_D_V, 64u * c, v4);
+                put(tile_l, 2 * MLA_D_V, 64u * c, l4);
+              } else {
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                  uint4 v4[4];
+#pragma unroll
+                  for (int u = 0; u < 4; ++u)
+                    v4[u] = make_uint4(__float_as_uint(__uint_as_float(o[16 * half + 4 * u + 0]) * inv),
+                                       __float_as_uint(__uint_as_float(o[16 * half + 4 * u + 1]) * inv),
+                                       __float_as_uint(__uint_as_float(o[16 * half + 4 * u + 2]) * inv),
+                                       __float_as_uint(__uint_as_float(o[16 * half + 4 * u + 3]) * inv));
+                  put(tile_f, 4 * MLA_D_V, 128u * c + 64u * half, v4);
+                }
+              }
+            }
+          } else {
+            const bool stores = lane < rows_here && slot_ok;
+            const size_t at = size_t(stores ? i : 0) * MLA_D_V;
+            uint4* dst_b = reinterpret_cast<uint4*>(tile_b + at);
+            uint4* dst_l = reinterpret_cast<uint4*>(tile_l + (tile_l != nullptr ? at : 0));
+            uint4* dst_f = reinterpret_cast<uint4*>(tile_f + (tile_f != nullptr ? at : 0));
+#pragma unroll 1
+            for (int c = 0; c < 16; ++c) {
+              uint32_t o[32];
+              tmem_ld32(tmem + lane_off + 32u * c, o);
+              tmem_wait_ld();
+              if (!stores) continue;
+              if (whole && tile_l == nullptr) {
+#pragma unroll
+                for (int u = 0; u < 4; ++u)
+                  dst_b[c * 4 + u] = make_uint4(
+                      pack_bf16(__uint_as_float(o[8 * u + 0]) * inv, __uint_as_float(o[8 * u + 1]) * inv),
+                      pack_bf16(__uint_as_float(o[8 * u + 2]) * inv, __uint_as_float(o[8 * u + 3]) * inv),
+                      pack_bf16(__uint_as_float(o[8 * u + 4]) * inv, __uint_as_float(o[8 * u + 5]) * inv),
+                      pack_bf16(__uint_as_float(o[8 * u + 6]) * inv, __uint_as_float(o[8 * u + 7]) * inv));
+              } else if (whole) {
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                  uint32_t hi[4], lo[4];
+#pragma unroll
+                  for (int k = 0; k < 4; ++k)
+                    split_bf16(__uint_as_float(o[8 * u + 2 * k]) * inv, __uint_as_float(o[8 * u + 2 * k + 1]) * inv,
+                               &hi[k], &lo[k]);
+                  dst_b[c * 4 + u] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                  dst_l[c * 4 + u] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                }
+              } else {
+#pragma unroll
+                for (int u = 0; u < 8; ++u)
+                  dst_f[c * 8 + u] = make_uint4(__float_as_uint(__uint_as_float(o[4 * u + 0]) * inv),
+                                                __float_as_uint(__uint_as_float(o[4 * u + 1]) * inv),
+                                                __float_as_uint(__uint_as_float(o[4 * u + 2]) * inv),
+                                                __float_as_uint(__uint_as_float(o[4 * u + 3]) * inv));
               }
             }
           }

@@ -281,3 +281,11 @@ def test_fp8_nan_in_unused_slots_and_pages():
     wl.kv_scale = torch.cat([scale, torch.full((1, 64), float("nan"))])
     O1, L1, st = run(wl)
     assert st == 0 and np.isfinite(O1).all() and np.array_equal(O0, O1) and np.array_equal(L0, L1)
+
+
+@pytest.mark.parametrize("cache", ["bf16", "fp8"])
+@pytest.mark.parametrize("rows", [31, 33, 95, 96, 97, 127, 129, 223, 225])
+def test_tiles_on_either_side_of_the_epilogues_swap(cache, rows):
+    # whole tiles and, with the long request, cut ones
+    check_full(mw.make(3, 1, rows, [700, 0, 64], seed=rows, cache_dtype=cache, name="swap_whole"))
+    check_full(mw.make(2, 1, rows, [70, 7000], seed=rows, cache_dtype=cache, name="swap_cut"))

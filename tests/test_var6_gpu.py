@@ -101,3 +101,15 @@ def test_var6_spec_shape_sampled():
     rows = [(0, 0), (0, 15), (13, 7), (31, 15)]
     ref, Lr = _reference(wl, q, k_new, v_new, wv, n, rows=rows)
     _assert_contract(np.stack([got[r, i] for r, i in rows]), np.stack([L[r, i] for r, i in rows]), ref, Lr)
+
+
+@pytest.mark.parametrize("heads", [16, 32, 95, 96, 97, 130])
+def test_var6_of_tiles_on_either_side_of_the_epilogues_swap(heads):
+    # the two-term output, whole and cut
+    wl = mw.make(2, 1, heads, [100, 6000], seed=heads, name="var6_swap")
+    g = torch.Generator().manual_seed(heads)
+    q = torch.randn(2, 1, heads, 192, generator=g).to(torch.bfloat16)
+    k_new, v_new = (torch.randn(2, 4, heads, 128, generator=g).to(torch.bfloat16) for _ in range(2))
+    wv = mw.make_projections(1, heads, seed=heads + 1).w_kvb2
+    got, L = _run(wl, q, k_new, v_new, wv, 4)
+    _assert_contract(got, L, *_reference(wl, q, k_new, v_new, wv, 4))
