@@ -2,12 +2,12 @@
 // launches behind the C ABI declared in include/mla.h.  Every check runs
 // before anything is enqueued; an error return means the stream is untouched.
 #include <cuda_runtime.h>
-#include <nvtx3/nvToolsExt.h>
 
 #include <cmath>
 #include <cstring>
 #include <mutex>
 
+#include "call_range.h"
 #include "decode_launch.cuh"
 #ifdef MLA_TEST_ENTRY_POINTS
 #include "test_entry.h"
@@ -57,16 +57,6 @@ using namespace mla;
 namespace {
 
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-
-// NVTX range around an entry point's host work (argument checks, tensor-map
-// encoding, launches), so a profiler's timeline names each call.  Costs a
-// few nanoseconds when no tool is attached.
-struct CallRange {
-  explicit CallRange(const char* name) { nvtxRangePushA(name); }
-  ~CallRange() { nvtxRangePop(); }
-  CallRange(const CallRange&) = delete;
-  CallRange& operator=(const CallRange&) = delete;
-};
 
 // Shape checks shared by every entry point.
 int check_shape(const mla_shape_t* s) {

@@ -4,10 +4,10 @@
 // most kNoAllocMaxTiles tiles; the schedule assigns whole tiles to workers
 // (schedule_whole_tiles_kernel), so no fp32 partial slot is ever needed.
 #include <cuda_runtime.h>
-#include <nvtx3/nvToolsExt.h>
 
 #include <mutex>
 
+#include "call_range.h"
 #include "decode_launch.cuh"
 
 namespace mla {
@@ -26,14 +26,6 @@ constexpr int kMaxDevices = 64;
 static __device__ __align__(256) uint8_t g_noalloc_scratch[kNoAllocScratchBytes];
 
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-
-// NVTX range around the call's host work (as for the other entry points).
-struct CallRange {
-  explicit CallRange(const char* name) { nvtxRangePushA(name); }
-  ~CallRange() { nvtxRangePop(); }
-  CallRange(const CallRange&) = delete;
-  CallRange& operator=(const CallRange&) = delete;
-};
 
 // Address of this device's scratch and its SM count, looked up once per
 // device (the first call on a device, which therefore must not be made while
