@@ -42,15 +42,15 @@ L2_FLUSH_BYTES = 256 << 20
 # for the kernel sources they were taken on: reported as null as soon as any
 # of them differs (checked by content hash at run time).
 TRAFFIC_SOURCES_SHA1 = {
-    "mla_latent_space_b200/csrc/decode_sm100.cu": "e5f6ba3dd37f8e5d54a697283fb82ee1480018a6",
+    "mla_latent_space_b200/csrc/decode_sm100.cu": "b396fa803e0064aeb5b13bf1164c384ce0a4f502",
     "mla_latent_space_b200/csrc/sm100_ptx.cuh": "a666c6fb95adecc45850f281b1be3ecacba5d16c",
     "mla_latent_space_b200/csrc/kernel_util.cuh": "b3f72c3cb1f09be8899208755a3eda87bfb3c5d1",
-    "mla_latent_space_b200/csrc/common.cuh": "797b62c6a10e623c883dccbc08d9ca1dae2215e3",
+    "mla_latent_space_b200/csrc/common.cuh": "73ac157ef38ef47b0a1ff3aeabc2fc32a1c708bf",
     "mla_latent_space_b200/csrc/decode_launch.cuh": "e64bf743c78208194d85090d84f93c37d7a51217",
 }
 TRAFFIC_BYTES = {
-    "dsv3_b64_h128_t4096_paged": 311572480 + 5057024,
-    "fp8_b64_h128_t32768": 1374679552 + 22463744,
+    "dsv3_b64_h128_t4096_paged": 311563008 + 4642304,
+    "fp8_b64_h128_t32768": 1375365632 + 22555392,
 }
 
 

@@ -26,8 +26,8 @@
  * Conventions shared by every call
  *  - All tensor pointers are DEVICE pointers owned by the caller.  The
  *    library never allocates device memory, never frees caller memory and
- *    never synchronises the stream (except mla_get_device_status, which
- *    says so).
+ *    never synchronises the stream (except the *_get_device_status calls,
+ *    which say so).
  *  - Every call takes the caller's cudaStream_t (passed as void*: NULL is
  *    the legacy default stream) and enqueues its work there.
  *  - Return value: MLA_OK (0) or a negative MLA_ERR_* code.  Arguments are
@@ -377,7 +377,8 @@ int mla_evict_select(int32_t batch, int32_t max_tokens, const float* weights, co
  * the accepted path of a drafted tree (src = its positions, base = the
  * committed length).  Rows that no destination covers are left as they were;
  * the caller then uses base + src_lens[r] as the request's length.
- *   shape   : the cache's (s_q and num_heads are not used).
+ *   shape   : the cache's (s_q and num_heads are checked as everywhere, but
+ *             not used).
  *   src     : int32 [batch, max_rows]; the first src_lens[r] of a row ascend
  *             strictly, with base + k <= src[r][k] < max_pages_per_seq * 64.
  *             An entry that does not, or whose page id is out of range, is

@@ -722,7 +722,7 @@ const char* mla_error_string(int code) {
     case MLA_ERR_WORKSPACE: return "MLA_ERR_WORKSPACE: schedule or workspace buffer too small";
     case MLA_ERR_CUDA: return "MLA_ERR_CUDA: a CUDA runtime call failed";
     case MLA_ERR_TIMEOUT: return "MLA_ERR_TIMEOUT: a bounded device wait gave up";
-    case MLA_ERR_DEVICE_CHECK: return "MLA_ERR_DEVICE_CHECK: out-of-range seqlen or page id, or a value row outside fp16 range, seen on the device";
+    case MLA_ERR_DEVICE_CHECK: return "MLA_ERR_DEVICE_CHECK: out-of-range seqlen, page id or list entry, or a value row outside fp16 range, seen on the device";
     default: return "MLA: unknown error code";
   }
 }

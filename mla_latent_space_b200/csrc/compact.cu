@@ -14,9 +14,10 @@
 // same.  Each row is read once and written once: what bounds it is HBM, as
 // long as enough rows are in flight: four CTAs an SM hold 36 KB each, and a
 // CTA resolves its next group's pages and search while the current rows are
-// on their way.  64 x 2048 of 4096 rows of BF16 (303 MB): 59 us; with a CTA a
-// group, handed out by a counter, 69.6; waiting for all earlier groups
-// instead of searching makes the CTAs queue behind each other: 94.
+// on their way.  64 x 2048 of 4096 rows of BF16 (303 MB): 61 us on the device,
+// 64 a call; with a CTA a group, handed out by a counter, 70 a call; waiting
+// for all earlier groups instead of searching makes the CTAs queue behind
+// each other: 94.
 //
 // Workspace: [status][finished CTAs][epoch] in the first 256 bytes, then a
 // word a group: the epoch of the last call that read its rows.  Epochs only
