@@ -30,9 +30,9 @@
 // so a row is one CTA's up to 8192 tokens and 400 more for each row of the
 // batch, or where the clusters would queue.  The host knows the rows' length,
 // not the requests': 64 requests of 4096 tokens in rows of 131072, which only
-// a cluster holds, take 22 us.  What bounds it is latency: of the 16 us of two rows of 131072 tokens, 3.5 are the trip to
-// memory, 5 the digits' passes with their cluster barriers, 5 the ordered
-// output.  (Adding up equal bins within a warp before the shared-memory adds,
+// a cluster holds, take 22 us.  What bounds it is latency: of the 16 us of two
+// rows of 131072 tokens, 3.5 are the trip to memory, 5 the digits' passes with
+// their cluster barriers, 5 the ordered output.  (Adding up equal bins within a warp before the shared-memory adds,
 // for the many weights that are zero, costs more than it saves: 30.7 us
 // against 26.6 at that stage.)
 #include <cooperative_groups.h>
